@@ -26,7 +26,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8q.so")
 LIB_DEBUG = os.path.join(HERE, "libfp8q_debug.so")
-SOURCES = ["quant_kernels.hip", "quant_mx.hip", "gemm_fp8.hip", "gemm_mx.hip", "api.cpp"]
+SOURCES = ["quant_kernels.hip", "quant_mx.hip", "gemm_fp8.hip", "gemm_mx.hip", "moe_route.hip", "moe_sort.hip", "moe_rows.hip",
+           "grad_clip.hip", "api.cpp"]
 ARCH = os.environ.get("FP8Q_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -596,3 +596,224 @@ fp8q_status fp8q_grouped_gemm_mx_dgrad(const uint8_t* dyq, const uint8_t* dys, c
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------- MoE routing
+namespace {
+
+// Rows accessed at any element alignment (the MoE row kernels).
+inline bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)n == 0; }
+
+fp8q_status check_rows(const void* p, fp8q_dtype t, int64_t ld, int64_t cols) {
+  if (!p) return FP8Q_ERR_NULL;
+  if (ld < cols) return FP8Q_ERR_STRIDE;
+  return aligned_to(p, esize(t)) ? FP8Q_OK : FP8Q_ERR_ALIGN;
+}
+
+fp8q_status check_route(fp8q_dtype lt, int64_t T, int64_t E, int k, int score, int renormalize, float scale) {
+  if (!valid_dtype(lt)) return FP8Q_ERR_DTYPE;
+  if (T < 0 || T > kMaxDim || E < 1 || E > fp8q::kMaxExperts || k < 1 || k > fp8q::kMaxTopK || k > E ||
+      T * k > kMaxDim)
+    return FP8Q_ERR_SHAPE;
+  if ((score != FP8Q_SOFTMAX && score != FP8Q_SIGMOID) || (renormalize != 0 && renormalize != 1) ||
+      !(scale - scale == 0.f))
+    return FP8Q_ERR_SHAPE;
+  return FP8Q_OK;
+}
+
+// The sizes of the row entry points: groups and 8-column pieces are counted
+// in 32 bits.
+fp8q_status check_moe_rows(fp8q_dtype t, int64_t T, int64_t H, int k) {
+  if (!valid_dtype(t)) return FP8Q_ERR_DTYPE;
+  if (T < 0 || H < 0 || T > kMaxDim || H > kMaxDim || k < 1 || k > fp8q::kMaxTopK || T * k > kMaxDim)
+    return FP8Q_ERR_SHAPE;
+  if (T * (cdiv(H, 8) + 15) > kMaxDim) return FP8Q_ERR_SHAPE;
+  return FP8Q_OK;
+}
+
+fp8q_status check_codes(const uint8_t* q, int64_t ld_q, const float* s, int64_t ld_s, int64_t H) {
+  if (!q || !s) return FP8Q_ERR_NULL;
+  if (ld_q < H || ld_s < cdiv(H, 128)) return FP8Q_ERR_STRIDE;
+  return aligned4(s) ? FP8Q_OK : FP8Q_ERR_ALIGN;
+}
+
+// The map of the row entry points lives on the device, as the expert offsets
+// do; the FP8Q_DEBUG build rejects one that is not a permutation of the rows.
+fp8q_status debug_check_dst(const int32_t* dst, int64_t m, hipStream_t stream) {
+#ifdef FP8Q_DEBUG
+  std::vector<int32_t> h((size_t)m);
+  if (hipMemcpyAsync(h.data(), dst, h.size() * sizeof(int32_t), hipMemcpyDeviceToHost, stream) != hipSuccess ||
+      hipStreamSynchronize(stream) != hipSuccess)
+    return FP8Q_ERR_LAUNCH;
+  std::vector<bool> seen((size_t)m, false);
+  for (const int32_t d : h) {
+    const int64_t r = d >= 0 ? (int64_t)d : -1 - (int64_t)d;
+    if (r >= m || seen[(size_t)r]) return FP8Q_ERR_SHAPE;
+    seen[(size_t)r] = true;
+  }
+#else
+  (void)dst; (void)m; (void)stream;
+#endif
+  return FP8Q_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8q_status fp8q_moe_route(const void* logits, fp8q_dtype lt, int64_t T, int64_t E, int64_t ld, int k, int score,
+                           const float* bias, int renormalize, float scale, int32_t* ids, float* weights,
+                           hipStream_t stream) {
+  if (const fp8q_status c = check_route(lt, T, E, k, score, renormalize, scale); c != FP8Q_OK || T == 0) return c;
+  if (const fp8q_status c = check_rows(logits, lt, ld, E); c != FP8Q_OK) return c;
+  if (!ids || !weights) return FP8Q_ERR_NULL;
+  if (!aligned4(ids) || !aligned4(weights) || !aligned4(bias)) return FP8Q_ERR_ALIGN;
+  const fp8q::MoeRoute a{logits, lt == FP8Q_BF16, score == FP8Q_SIGMOID, renormalize == 1, T, E, ld, k, scale};
+  return launched(fp8q::launch_moe_route(a, bias, ids, weights, stream));
+}
+
+fp8q_status fp8q_moe_route_bwd(const float* dweights, const void* logits, fp8q_dtype lt, int64_t T, int64_t E,
+                               int64_t ld, const int32_t* ids, int k, int score, int renormalize, float scale,
+                               void* dlogits, int64_t ld_d, hipStream_t stream) {
+  if (const fp8q_status c = check_route(lt, T, E, k, score, renormalize, scale); c != FP8Q_OK || T == 0) return c;
+  if (const fp8q_status c = check_rows(logits, lt, ld, E); c != FP8Q_OK) return c;
+  if (const fp8q_status c = check_rows(dlogits, lt, ld_d, E); c != FP8Q_OK) return c;
+  if (!dweights || !ids) return FP8Q_ERR_NULL;
+  if (!aligned4(dweights) || !aligned4(ids)) return FP8Q_ERR_ALIGN;
+  const fp8q::MoeRoute a{logits, lt == FP8Q_BF16, score == FP8Q_SIGMOID, renormalize == 1, T, E, ld, k, scale};
+  return launched(fp8q::launch_moe_route_bwd(a, dweights, ids, dlogits, ld_d, stream));
+}
+
+int64_t fp8q_moe_sort_workspace(int64_t M, int64_t E) {
+  if (M < 0 || M > kMaxDim || E < 1 || E > fp8q::kMaxExperts) return -1;
+  return fp8q::moe_sort_workspace(M, E);
+}
+
+fp8q_status fp8q_moe_sort(const int32_t* ids, int64_t M, int64_t E, int cover, int32_t* offsets, int32_t* dst,
+                          int32_t* src, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (M < 0 || M > kMaxDim || E < 1 || E > fp8q::kMaxExperts || (cover != 0 && cover != 1)) return FP8Q_ERR_SHAPE;
+  if (!offsets || (M > 0 && (!ids || !dst))) return FP8Q_ERR_NULL;
+  if (!aligned4(ids) || !aligned4(offsets) || !aligned4(dst) || !aligned4(src)) return FP8Q_ERR_ALIGN;
+  const int64_t need = fp8q::moe_sort_workspace(M, E);
+  if (need > 0) {
+    if (!workspace) return FP8Q_ERR_NULL;
+    if (!aligned4(workspace)) return FP8Q_ERR_ALIGN;
+    if (workspace_bytes < need) return FP8Q_ERR_SHAPE;
+  }
+  return launched(fp8q::launch_moe_sort(ids, M, E, cover == 1, offsets, dst, src, workspace, stream));
+}
+
+fp8q_status fp8q_moe_dispatch(const void* x, fp8q_dtype xt, int64_t T, int64_t H, int64_t ld_x, const int32_t* dst,
+                              int k, void* rows, int64_t ld_rows, uint8_t* q, int64_t ld_q, float* scale,
+                              int64_t ld_s, hipStream_t stream) {
+  if (const fp8q_status c = check_moe_rows(xt, T, H, k); c != FP8Q_OK || T == 0 || H == 0) return c;
+  if (const fp8q_status c = check_rows(x, xt, ld_x, H); c != FP8Q_OK) return c;
+  if (!dst || (!rows && !q)) return FP8Q_ERR_NULL;
+  if (!aligned4(dst)) return FP8Q_ERR_ALIGN;
+  if (rows)
+    if (const fp8q_status c = check_rows(rows, xt, ld_rows, H); c != FP8Q_OK) return c;
+  if (q)
+    if (const fp8q_status c = check_codes(q, ld_q, scale, ld_s, H); c != FP8Q_OK) return c;
+  if (const fp8q_status c = debug_check_dst(dst, T * k, stream); c != FP8Q_OK) return c;
+  const fp8q::MoeRows a{xt == FP8Q_BF16, T, k, H, dst, rows, ld_rows, q, ld_q, scale, ld_s};
+  return launched(fp8q::launch_moe_dispatch(a, x, ld_x, stream));
+}
+
+fp8q_status fp8q_moe_dispatch_bwd(const void* drows, fp8q_dtype t, int64_t T, int64_t H, int64_t ld_rows,
+                                  const int32_t* dst, int k, void* dx, int64_t ld_dx, hipStream_t stream) {
+  if (const fp8q_status c = check_moe_rows(t, T, H, k); c != FP8Q_OK || T == 0 || H == 0) return c;
+  if (const fp8q_status c = check_rows(drows, t, ld_rows, H); c != FP8Q_OK) return c;
+  if (const fp8q_status c = check_rows(dx, t, ld_dx, H); c != FP8Q_OK) return c;
+  if (!dst) return FP8Q_ERR_NULL;
+  if (!aligned4(dst)) return FP8Q_ERR_ALIGN;
+  if (const fp8q_status c = debug_check_dst(dst, T * k, stream); c != FP8Q_OK) return c;
+  const fp8q::MoeRows a{t == FP8Q_BF16, T, k, H, dst, const_cast<void*>(drows), ld_rows, nullptr, 0, nullptr, 0};
+  return launched(fp8q::launch_moe_gather(a, nullptr, dx, ld_dx, stream));
+}
+
+fp8q_status fp8q_moe_combine(const void* yp, fp8q_dtype t, int64_t T, int64_t H, int64_t ld_yp, const int32_t* dst,
+                             int k, const float* weights, void* y, int64_t ld_y, hipStream_t stream) {
+  if (const fp8q_status c = check_moe_rows(t, T, H, k); c != FP8Q_OK || T == 0 || H == 0) return c;
+  if (const fp8q_status c = check_rows(yp, t, ld_yp, H); c != FP8Q_OK) return c;
+  if (const fp8q_status c = check_rows(y, t, ld_y, H); c != FP8Q_OK) return c;
+  if (!dst || !weights) return FP8Q_ERR_NULL;
+  if (!aligned4(dst) || !aligned4(weights)) return FP8Q_ERR_ALIGN;
+  if (const fp8q_status c = debug_check_dst(dst, T * k, stream); c != FP8Q_OK) return c;
+  const fp8q::MoeRows a{t == FP8Q_BF16, T, k, H, dst, const_cast<void*>(yp), ld_yp, nullptr, 0, nullptr, 0};
+  return launched(fp8q::launch_moe_gather(a, weights, y, ld_y, stream));
+}
+
+fp8q_status fp8q_moe_combine_bwd(const void* dy, const void* yp, fp8q_dtype t, int64_t T, int64_t H, int64_t ld_dy,
+                                 int64_t ld_yp, const int32_t* dst, int k, const float* weights, void* rows,
+                                 int64_t ld_rows, uint8_t* q, int64_t ld_q, float* scale, int64_t ld_s,
+                                 float* dweights, hipStream_t stream) {
+  if (const fp8q_status c = check_moe_rows(t, T, H, k); c != FP8Q_OK || T == 0) return c;
+  if (!dst || !weights || !dweights) return FP8Q_ERR_NULL;
+  if (H > 0) {
+    if (!rows && !q) return FP8Q_ERR_NULL;
+    if (const fp8q_status c = check_rows(dy, t, ld_dy, H); c != FP8Q_OK) return c;
+    if (const fp8q_status c = check_rows(yp, t, ld_yp, H); c != FP8Q_OK) return c;
+    if (rows)
+      if (const fp8q_status c = check_rows(rows, t, ld_rows, H); c != FP8Q_OK) return c;
+    if (q)
+      if (const fp8q_status c = check_codes(q, ld_q, scale, ld_s, H); c != FP8Q_OK) return c;
+  }
+  if (!aligned4(dst) || !aligned4(weights) || !aligned4(dweights)) return FP8Q_ERR_ALIGN;
+  if (const fp8q_status c = debug_check_dst(dst, T * k, stream); c != FP8Q_OK) return c;
+  const fp8q::MoeRows a{t == FP8Q_BF16, T, k, H, dst, rows, ld_rows, q, ld_q, scale, ld_s};
+  return launched(fp8q::launch_moe_combine_bwd(a, dy, ld_dy, yp, ld_yp, weights, dweights, stream));
+}
+
+int64_t fp8q_grad_clip_workspace(int64_t n) {
+  if (n < 0 || n > kMaxDim) return -1;
+  return cdiv(n, fp8q::kMaxClipTensors) * fp8q::kClipBlocks * (int64_t)sizeof(double);
+}
+
+fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, double max_norm, void* workspace,
+                           int64_t workspace_bytes, float* norm, hipStream_t stream) {
+  if (!valid_dtype(ot)) return FP8Q_ERR_DTYPE;
+  if (n < 0 || n > kMaxDim || !(max_norm >= 0.0)) return FP8Q_ERR_SHAPE;
+  if (!norm || (n > 0 && (!grads || !workspace))) return FP8Q_ERR_NULL;
+  if (!aligned4(norm) || !aligned_to(workspace, 8)) return FP8Q_ERR_ALIGN;
+  if (workspace_bytes < fp8q_grad_clip_workspace(n)) return FP8Q_ERR_SHAPE;
+  int64_t chunks = 0;  // of all tensors: counted in 32 bits
+  for (int64_t i = 0; i < n; ++i) {
+    const fp8q_grad& g = grads[i];
+    if (g.len < 0 || (chunks += fp8q::clip_chunks(g.len)) > kMaxDim / 2) return FP8Q_ERR_SHAPE;
+    if (g.len == 0) continue;
+    if (!g.g || !g.out) return FP8Q_ERR_NULL;
+    if (!aligned4(g.g) || !aligned_to(g.out, esize(ot))) return FP8Q_ERR_ALIGN;
+  }
+  // tables of up to kMaxClipTensors non-empty tensors, one launch each and pass
+  const bool bf16 = ot == FP8Q_BF16;
+  double* const part = static_cast<double*>(workspace);
+  int parts = 0;
+  fp8q::ClipBatch b;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t i = 0;
+    bool first = true;
+    do {
+      b.n = 0;
+      b.cum[0] = 0;
+      for (; i < n && b.n < fp8q::kMaxClipTensors; ++i) {
+        const int64_t c = fp8q::clip_chunks(grads[i].len);
+        if (c == 0) continue;
+        b.g[b.n] = grads[i].g; b.out[b.n] = grads[i].out; b.len[b.n] = grads[i].len;
+        b.cum[b.n + 1] = b.cum[b.n] + (int)c;
+        ++b.n;
+      }
+      hipError_t e = hipSuccess;
+      if (pass == 0) {
+        int blocks = 0;
+        if (b.n > 0) e = fp8q::launch_grad_sumsq(b, part + parts, &blocks, stream);
+        parts += blocks;
+      } else if (b.n > 0 || first) {
+        e = fp8q::launch_grad_scale(b, bf16, part, parts, max_norm, first ? norm : nullptr, stream);
+      }
+      if (e != hipSuccess) return FP8Q_ERR_LAUNCH;
+      first = false;
+    } while (i < n);
+  }
+  return FP8Q_OK;
+}
+
+}  // extern "C"

@@ -126,4 +126,59 @@ struct MxArgs {
 };
 hipError_t launch_gemm_mx(const MxArgs& a, hipStream_t st);
 
+// ------------------------------------------------------------ MoE routing
+constexpr int kMaxExperts = 1024;  // router and sort (their tables live in LDS)
+constexpr int kMaxTopK = 32;       // choices per token
+
+// Router: logits [tokens, experts] (row stride ld elements), k choices.
+struct MoeRoute {
+  const void* logits;
+  bool bf16, sigmoid, renorm;
+  int64_t tokens, experts, ld, k;
+  float scale;
+};
+hipError_t launch_moe_route(const MoeRoute& a, const float* bias, int32_t* ids, float* w, hipStream_t st);
+hipError_t launch_moe_route_bwd(const MoeRoute& a, const float* dw, const int32_t* ids, void* dl, int64_t ld_dl,
+                                hipStream_t st);
+
+// Stable counting sort of n pairs into e bins and one of dropped pairs; ws of
+// moe_sort_workspace(n, e) bytes.
+int64_t moe_sort_workspace(int64_t n, int64_t e);
+hipError_t launch_moe_sort(const int32_t* ids, int64_t n, int64_t e, bool cover, int32_t* offsets, int32_t* dst,
+                           int32_t* src, void* ws, hipStream_t st);
+
+// Rows in expert order [tokens * k, cols] and the map to them (moe_rows.hip);
+// rows or q may be NULL where an output is not wanted.
+struct MoeRows {
+  bool bf16;
+  int64_t tokens, k, cols;
+  const int32_t* dst;  // [tokens, k]
+  void* rows;
+  int64_t ld_rows;
+  uint8_t* q;
+  int64_t ld_q;
+  float* s;
+  int64_t ld_s;
+};
+hipError_t launch_moe_dispatch(const MoeRows& a, const void* x, int64_t ld_x, hipStream_t st);
+// y[t] = sum_j w[t, j] rows[dst[t, j]] (w == NULL: the plain sum)
+hipError_t launch_moe_gather(const MoeRows& a, const float* w, void* y, int64_t ld_y, hipStream_t st);
+hipError_t launch_moe_combine_bwd(const MoeRows& a, const void* dy, int64_t ld_dy, const void* yp, int64_t ld_yp,
+                                  const float* w, float* dw, hipStream_t st);
+
+// ------------------------------------------------------- gradient clipping
+constexpr int kMaxClipTensors = 96;  // per launch: the table travels in the kernel's arguments
+constexpr int kClipBlocks = 2048;    // most blocks, and partial sums, per launch
+struct ClipBatch {
+  int n;
+  int cum[kMaxClipTensors + 1];  // first chunk of each tensor, then their number
+  const float* g[kMaxClipTensors];
+  void* out[kMaxClipTensors];
+  int64_t len[kMaxClipTensors];
+};
+int64_t clip_chunks(int64_t len);  // chunks a tensor is cut into
+hipError_t launch_grad_sumsq(const ClipBatch& b, double* part, int* blocks, hipStream_t st);
+hipError_t launch_grad_scale(const ClipBatch& b, bool out_bf16, const double* part, int parts, double max_norm,
+                             float* norm, hipStream_t st);
+
 }  // namespace fp8q

@@ -39,7 +39,8 @@
  *     re-entrant and thread-safe.  Buffers must stay valid
  *     until the work enqueued on `stream` has completed.
  *   - Work is enqueued asynchronously on `stream` (NULL = the default
- *     stream).  Results are deterministic (no atomics, no split-K).
+ *     stream).  Results are deterministic (no split-K, no atomics but integer
+ *     counts, whose sums do not depend on their order).
  *   - The FP8 and MX GEMMs pick a 256x128 or a 256x256 workgroup tile by
  *     problem size (the wide one when its grid has more tiles than half the
  *     device's compute units and the output width is a multiple of 256).
@@ -507,6 +508,134 @@ fp8q_status fp8q_grouped_gemm_mx_dgrad(const uint8_t* dyq, const uint8_t* dys, c
                                        const uint8_t* ws_t, const int32_t* offsets, int64_t E, int64_t M_total,
                                        int64_t N, int64_t K, void* dx, fp8q_dtype dxt, int64_t ld_dx,
                                        hipStream_t stream);
+
+/*
+ * ---- MoE routing: from a router's logits to rows in expert order and back.
+ *
+ * T tokens choose k of E experts each; pair p = t*k + j is token t's j-th
+ * choice and M = T*k the number of rows.  The grouped products above take the
+ * rows in expert order; these entry points make that order and undo it, with
+ * the gradients of each step.  Limits: 1 <= k <= 32, k <= E <= 1024.
+ * Logits, token rows and expert rows may start at any element and have any
+ * row stride >= their length (no 16-byte rule here); ids, weights and maps
+ * are contiguous [T, k].  Codes written with a row stride that is a multiple
+ * of 16 bytes feed the grouped products and quantizers as they are.
+ */
+typedef enum { FP8Q_SOFTMAX = 0, FP8Q_SIGMOID = 1 } fp8q_score;
+
+/*
+ * Router: the k best experts of every token and their weights.
+ *   logits  : [T, E] of type lt, row stride ld; -inf masks an expert for a token
+ *   score   : fp8q_score; s = softmax(logits) over the E experts, or sigmoid
+ *   bias    : optional [E] finite FP32, added to the score for the CHOICE only
+ *             (load balancing), or NULL.  The choice is by logit without it
+ *             and by s + bias, both in 64 bits, with it; ties go to the lower
+ *             expert.
+ *   renormalize : 1 divides the chosen scores by their sum (their ratios hold
+ *             where the scores themselves vanish in FP32)
+ *   scale   : finite factor of the weights
+ *   ids     : [T, k] int32, best first; -1 where a token has fewer than k
+ *             experts that are not masked
+ *   weights : [T, k] FP32: chosen score (renormalized) * scale, 0 beside id -1
+ * A NaN logit is never chosen (softmax weights of its token are NaN).
+ */
+fp8q_status fp8q_moe_route(const void* logits, fp8q_dtype lt, int64_t T, int64_t E, int64_t ld, int k, int score,
+                           const float* bias, int renormalize, float scale, int32_t* ids, float* weights,
+                           hipStream_t stream);
+
+/*
+ * Gradient of fp8q_moe_route's weights to the logits, for the ids it chose
+ * (the choice itself has no gradient).  p = score, g = dweights * scale:
+ *   softmax              dl_e = p_e (g_e - sum_j g_j p_j), g_e = 0 if not chosen
+ *   softmax, renormalized  dl_j = w_j (g_j - sum g w), w_j = p_j / sum of chosen p
+ *   sigmoid              dl_j = g_j p_j (1 - p_j)
+ *   sigmoid, renormalized  dl_j = w_j (1 - p_j) (g_j - sum g w)
+ * (the last three are 0 for experts not chosen).  Every entry of dlogits
+ * [T, E] (type lt, row stride ld_d) is written.  A token's ids differ from
+ * each other; entries outside [0, E) are no choice.
+ */
+fp8q_status fp8q_moe_route_bwd(const float* dweights, const void* logits, fp8q_dtype lt, int64_t T, int64_t E,
+                               int64_t ld, const int32_t* ids, int k, int score, int renormalize, float scale,
+                               void* dlogits, int64_t ld_d, hipStream_t stream);
+
+/*
+ * Stable sort of M pairs by expert.
+ *   ids     : [M] int32; a pair whose id is outside [0, E) is dropped
+ *   offsets : [E+1]; expert e's rows are [offsets[e], offsets[e+1]).  cover = 0:
+ *             offsets[E] is the number of pairs kept.  cover = 1: offsets[E] = M,
+ *             the dropped pairs' rows count as the last expert's; they are rows
+ *             of zeros (see fp8q_moe_dispatch), so every product over them adds
+ *             zeros, and the grouped entry points' rule offsets[E] = M_total
+ *             holds without a host read.
+ *   dst     : [M]; row of pair p, or -1 - row if it is dropped.  Dropped pairs
+ *             take the rows after the kept ones, all in pair order, so the rows
+ *             are a permutation of [0, M).
+ *   src     : optional [M], the pair of each row (the inverse map), or NULL
+ *   workspace : fp8q_moe_sort_workspace(M, E) bytes (NULL if that is 0)
+ */
+fp8q_status fp8q_moe_sort(const int32_t* ids, int64_t M, int64_t E, int cover, int32_t* offsets, int32_t* dst,
+                          int32_t* src, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+/* Bytes of workspace that call needs (-1: sizes out of range). */
+int64_t fp8q_moe_sort_workspace(int64_t M, int64_t E);
+
+/*
+ * Token rows into expert order: row r of pair (t, j) becomes x[t], or zeros if
+ * the pair is dropped.
+ *   x    : [T, H] of type xt, row stride ld_x
+ *   dst  : [T, k] DEVICE map of fp8q_moe_sort (not checked by the product
+ *          library: entries that name no row are skipped; the FP8Q_DEBUG build
+ *          rejects a map that is no permutation, FP8Q_ERR_SHAPE)
+ *   rows : [M, H] of type xt, row stride ld_rows, or NULL
+ *   q, scale : [M, H] codes and [M, ceil(H/128)] scales of those rows, bit for
+ *          bit what fp8q_quant_act_1x128 makes of them, or NULL
+ * At least one of rows and q is wanted.  A token is read and quantized once.
+ */
+fp8q_status fp8q_moe_dispatch(const void* x, fp8q_dtype xt, int64_t T, int64_t H, int64_t ld_x, const int32_t* dst,
+                              int k, void* rows, int64_t ld_rows, uint8_t* q, int64_t ld_q, float* scale,
+                              int64_t ld_s, hipStream_t stream);
+
+/* Its gradient: dx[t] = sum over token t's kept pairs, in order and in FP32, of
+ * drows[dst[t, j]]; rounded once to dx's type t. */
+fp8q_status fp8q_moe_dispatch_bwd(const void* drows, fp8q_dtype t, int64_t T, int64_t H, int64_t ld_rows,
+                                  const int32_t* dst, int k, void* dx, int64_t ld_dx, hipStream_t stream);
+
+/* Expert rows back into token order: y[t] = sum over token t's kept pairs, in
+ * order and in FP32, of weights[t, j] * yp[dst[t, j]]; rounded once. */
+fp8q_status fp8q_moe_combine(const void* yp, fp8q_dtype t, int64_t T, int64_t H, int64_t ld_yp, const int32_t* dst,
+                             int k, const float* weights, void* y, int64_t ld_y, hipStream_t stream);
+
+/*
+ * Its gradients, from one read of dy and of yp:
+ *   rows     : [M, H] of type t, or NULL: weights[t, j] * dy[t] rounded to t at
+ *              row dst[t, j], zeros at a dropped pair's row
+ *   q, scale : codes and scales of those (rounded) rows, or NULL
+ *   dweights : [T, k] FP32, dy[t] . yp[dst[t, j]], 0 for a dropped pair
+ */
+fp8q_status fp8q_moe_combine_bwd(const void* dy, const void* yp, fp8q_dtype t, int64_t T, int64_t H, int64_t ld_dy,
+                                 int64_t ld_yp, const int32_t* dst, int k, const float* weights, void* rows,
+                                 int64_t ld_rows, uint8_t* q, int64_t ld_q, float* scale, int64_t ld_s,
+                                 float* dweights, hipStream_t stream);
+
+/*
+ * Gradient clipping by the global norm: norm = sqrt(sum of g^2 over all
+ * tensors), formed in 64 bits, and out = g * c, c = 1 if norm <= max_norm, else
+ * max_norm / norm (so a NaN norm gives NaN, an infinite one zeros and NaN).
+ *   grads : HOST array (read during the call only) of n dense FP32 tensors of
+ *           any length; out is of type ot, and may be g itself if ot is FP32
+ *   max_norm : >= 0; +inf only measures and copies
+ *   workspace : 8-byte aligned, fp8q_grad_clip_workspace(n) bytes
+ *   norm  : one FP32, the norm before clipping
+ * n = 0 gives norm 0.  Tensors must not overlap each other.
+ */
+typedef struct {
+  const float* g;
+  void* out;
+  int64_t len;
+} fp8q_grad;
+fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, double max_norm, void* workspace,
+                           int64_t workspace_bytes, float* norm, hipStream_t stream);
+/* Bytes of workspace that call needs (-1: n out of range). */
+int64_t fp8q_grad_clip_workspace(int64_t n);
 
 #ifdef __cplusplus
 }
