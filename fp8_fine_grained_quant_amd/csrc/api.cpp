@@ -620,13 +620,13 @@ fp8q_status check_route(fp8q_dtype lt, int64_t T, int64_t E, int k, int score, i
   return FP8Q_OK;
 }
 
-// The sizes of the row entry points: groups and 8-column pieces are counted
-// in 32 bits.
+// The sizes of the row entry points: columns, groups and 8-column pieces are
+// counted in 32 bits, past a row's end too.
 fp8q_status check_moe_rows(fp8q_dtype t, int64_t T, int64_t H, int k) {
   if (!valid_dtype(t)) return FP8Q_ERR_DTYPE;
   if (T < 0 || H < 0 || T > kMaxDim || H > kMaxDim || k < 1 || k > fp8q::kMaxTopK || T * k > kMaxDim)
     return FP8Q_ERR_SHAPE;
-  if (T * (cdiv(H, 8) + 15) > kMaxDim) return FP8Q_ERR_SHAPE;
+  if (H > kMaxDim / 2 || T * (cdiv(H, 8) + 15) > kMaxDim) return FP8Q_ERR_SHAPE;
   return FP8Q_OK;
 }
 

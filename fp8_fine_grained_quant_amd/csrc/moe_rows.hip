@@ -20,212 +20,356 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kJ = 8;  // choices handled together: 8 row loads in flight per lane
+constexpr int kJ = 8;              // choices handled together: 8 row loads in flight per lane
+constexpr int kWideThreads = 512;  // most threads of a block that works on one token
 
 __device__ __forceinline__ bool row_ok(int r, int m) { return (uint32_t)r < (uint32_t)m; }
 
-// ---------------------------------------------------------------------------
-// Dispatch: 16 lanes own one 128-column group of one token, 8 columns per
-// lane, so the group's max-abs is one DPP row reduction (as k_quant_act) and
-// a token is read and quantized once however many rows it goes to.
-template <class Row, bool ROWS, bool CODES>
-__global__ __launch_bounds__(256) void k_dispatch(const typename Row::elem* __restrict__ x, int64_t ld_x,
-                                                  const int* __restrict__ dst, int k, int m,
-                                                  typename Row::elem* __restrict__ rows, int64_t ld_r,
-                                                  uint8_t* __restrict__ q, int64_t ld_q, float* __restrict__ s,
-                                                  int64_t ld_s, int cols, int ngr, int total) {
-  const int g = (int)((blockIdx.x * 256u + threadIdx.x) >> 4);
-  const int lig = threadIdx.x & 15;
-  if (g >= total) return;
-  const int t = g / ngr, c = g - t * ngr;
-  const int c0 = c * 128 + lig * 8;
-  float v[8];
-  load_cols<Row>(x + (int64_t)t * ld_x, c0, cols, v);
-  uint32_t w0 = 0, w1 = 0;
-  float sc = 0.f;
-  if (CODES) {
-    uint32_t a = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a = max(a, abs_bits(v[e]));
-    a = row16_max_u32(a);
-    float inv;
-    group_scale(__uint_as_float(a), sc, inv);
-    w0 = pack4_e4m3_grp(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-    w1 = pack4_e4m3_grp(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+// 16 lanes handle a 128-column group of a row, 8 columns each.  WIDE rows (a
+// wave's 512 columns or more) give a block to one token, or to a slice of its
+// columns, so the map's entries are uniform: they come by scalar loads and a
+// dropped pair is a uniform branch.  Narrow rows put several tokens into a
+// wave.  piece counts a token's lanes.
+template <bool WIDE>
+__device__ __forceinline__ void place(int per_token, int& t, int& piece) {
+  if (WIDE) {
+    t = (int)(blockIdx.x / (uint32_t)per_token);
+    piece = ((int)blockIdx.x - t * per_token) * (int)blockDim.x + (int)threadIdx.x;
+  } else {
+    const uint32_t i = blockIdx.x * 256u + threadIdx.x;
+    t = (int)(i / (uint32_t)per_token);
+    piece = (int)(i - (uint32_t)t * (uint32_t)per_token);
   }
+}
+
+// First column of a piece.
+template <class Row>
+__device__ __forceinline__ int piece_col(int piece) { return (piece >> 4) * 128 + (piece & 15) * Row::kLen; }
+
+// ---------------------------------------------------------------------------
+// Dispatch: 16 lanes own one 128-column group of one token, so the group's
+// max-abs is one DPP row reduction (as k_quant_act) and a token is read and
+// quantized once however many rows it goes to.
+template <class Row, bool ROWS, bool CODES, bool WIDE, int NT>
+__global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_dispatch(
+    const typename Row::elem* __restrict__ x, int64_t ld_x, const int* __restrict__ dst, int tokens, int k, int m,
+    typename Row::elem* __restrict__ rows, int64_t ld_r, uint8_t* __restrict__ q, int64_t ld_q,
+    float* __restrict__ s, int64_t ld_s, int cols, int per_token) {
+  int t, piece;
+  place<WIDE>(per_token, t, piece);
+  const int c = piece >> 4, c0 = piece_col<Row>(piece);
+  if (t >= tokens || c * 128 >= cols) return;
   const int* d = dst + (int64_t)t * k;
-  for (int j = 0; j < k; ++j) {
-    const int dj = d[j];
-    const bool kept = dj >= 0;
-    const int r = kept ? dj : -1 - dj;
-    if (!row_ok(r, m)) continue;
-    if (ROWS) {
-      float z[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = kept ? v[e] : 0.f;
-      store_cols<Row>(rows + (int64_t)r * ld_r, c0, cols, z);
-    }
+  auto body = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    const typename Row::Raw raw = load_piece<Row, kWhole, 0>(x + (int64_t)t * ld_x, c0, cols);
+    uint32_t w0 = 0, w1 = 0;
+    float sc = 0.f;
     if (CODES) {
-      store_codes(q + (int64_t)r * ld_q, c0, cols, kept ? w0 : 0u, kept ? w1 : 0u);
-      if (lig == 0) s[(int64_t)r * ld_s + c] = kept ? sc : kAmaxFloor / kFp8Max;
+      // a run outside holds values of its own group's last columns: they do not
+      // change the group's max-abs
+      float v[8];
+      Row::unpack(raw, v);
+      uint32_t a = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a = max(a, abs_bits(v[e]));
+      a = row16_max_u32(a);
+      float inv;
+      group_scale(__uint_as_float(a), sc, inv);
+      w0 = pack4_e4m3_grp(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+      w1 = pack4_e4m3_grp(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
     }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Weighted (W) or plain sum of a token's rows: one lane per 8 columns.
-template <class Row, bool W>
-__global__ __launch_bounds__(256) void k_gather(const typename Row::elem* __restrict__ rows, int64_t ld_r,
-                                                const int* __restrict__ dst, const float* __restrict__ w, int k,
-                                                int m, typename Row::elem* __restrict__ y, int64_t ld_y, int cols,
-                                                int nch, int total) {
-  const int i = (int)(blockIdx.x * 256u + threadIdx.x);
-  if (i >= total) return;
-  const int t = i / nch, c0 = (i - t * nch) * 8;
-  float acc[8];
+    for (int j0 = 0; j0 < k; j0 += kJ) {
+      int dj[kJ];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  const int64_t p0 = (int64_t)t * k;
-  for (int j = 0; j < k; ++j) {
-    const int r = dst[p0 + j];
-    if (!row_ok(r, m)) continue;
-    const float wj = W ? w[p0 + j] : 1.f;
-    float v[8];
-    load_cols<Row>(rows + (int64_t)r * ld_r, c0, cols, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = W ? __builtin_fmaf(wj, v[e], acc[e]) : acc[e] + v[e];
-  }
-  store_cols<Row>(y + (int64_t)t * ld_y, c0, cols, acc);
-}
-
-// ---------------------------------------------------------------------------
-// Combine backward: one block per token, so that a token's dw is summed
-// inside one block (no atomics; the order is fixed).
-template <class Row, bool ROWS, bool CODES>
-__global__ __launch_bounds__(256) void k_combine_bwd(const typename Row::elem* __restrict__ dy, int64_t ld_dy,
-                                                     const typename Row::elem* __restrict__ yp, int64_t ld_yp,
-                                                     const int* __restrict__ dst, const float* __restrict__ w, int k,
-                                                     int m, typename Row::elem* __restrict__ rows, int64_t ld_r,
-                                                     uint8_t* __restrict__ q, int64_t ld_q, float* __restrict__ s,
-                                                     int64_t ld_s, float* __restrict__ dw, int cols, int ngr) {
-  __shared__ float red[4][kJ];
-  const int t = (int)blockIdx.x, tid = threadIdx.x, lig = tid & 15;
-  const int64_t p0 = (int64_t)t * k;
-  for (int j0 = 0; j0 < k; j0 += kJ) {
-    const int nj = min(kJ, k - j0);
-    float acc[kJ];
-#pragma unroll
-    for (int u = 0; u < kJ; ++u) acc[u] = 0.f;
-    for (int c = tid >> 4; c < ngr; c += 16) {
-      const int c0 = c * 128 + lig * 8;
-      float g[8];
-      load_cols<Row>(dy + (int64_t)t * ld_dy, c0, cols, g);
+      for (int u = 0; u < kJ; ++u) dj[u] = d[min(j0 + u, k - 1)];
 #pragma unroll
       for (int u = 0; u < kJ; ++u) {
-        if (u >= nj) break;
-        const int d = dst[p0 + j0 + u];
-        const bool kept = d >= 0;
-        const int r = kept ? d : -1 - d;
+        if (j0 + u >= k) break;
+        const bool kept = dj[u] >= 0;
+        const int r = kept ? dj[u] : -1 - dj[u];
+        if (!row_ok(r, m)) continue;
+        if (ROWS) {
+          typename Row::Raw z{};
+          if (kept) z = raw;
+          store_piece<Row, kWhole, NT>(rows + (int64_t)r * ld_r, c0, cols, z);
+        }
+        if (CODES) {
+          store_codes<Row, kWhole, NT>(q + (int64_t)r * ld_q, c0, cols, kept ? w0 : 0u, kept ? w1 : 0u);
+          if ((piece & 15) == 0) s[(int64_t)r * ld_s + c] = kept ? sc : kAmaxFloor / kFp8Max;
+        }
+      }
+    }
+  };
+  if (no_cut<Row>(c0, cols)) body(std::true_type{}); else body(std::false_type{});
+}
+
+// ---------------------------------------------------------------------------
+// Weighted (W) or plain sum of a token's rows; up to kJ rows in flight.
+template <class Row, bool W, bool WIDE, int NT>
+__global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_gather(
+    const typename Row::elem* __restrict__ rows, int64_t ld_r, const int* __restrict__ dst,
+    const float* __restrict__ w, int tokens, int k, int m, typename Row::elem* __restrict__ y, int64_t ld_y, int cols,
+    int per_token) {
+  int t, piece;
+  place<WIDE>(per_token, t, piece);
+  const int c0 = piece_col<Row>(piece);
+  if (t >= tokens || (piece >> 4) * 128 >= cols) return;
+  const int64_t p0 = (int64_t)t * k;
+  auto body = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int j0 = 0; j0 < k; j0 += kJ) {
+      int r[kJ];
+      float wj[kJ];
+      typename Row::Raw raw[kJ];
+#pragma unroll
+      for (int u = 0; u < kJ; ++u) {
+        const int64_t at = p0 + min(j0 + u, k - 1);
+        r[u] = j0 + u < k ? dst[at] : -1;
+        wj[u] = W ? w[at] : 1.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kJ; ++u)
+        if (row_ok(r[u], m)) raw[u] = load_piece<Row, kWhole, NT>(rows + (int64_t)r[u] * ld_r, c0, cols);
+#pragma unroll
+      for (int u = 0; u < kJ; ++u)
+        if (row_ok(r[u], m)) {
+          float v[8];
+          Row::unpack(raw[u], v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = W ? __builtin_fmaf(wj[u], v[e], acc[e]) : acc[e] + v[e];
+        }
+    }
+    store_piece<Row, kWhole, 0>(y + (int64_t)t * ld_y, c0, cols, Row::pack(acc));
+  };
+  if (no_cut<Row>(c0, cols)) body(std::true_type{}); else body(std::false_type{});
+}
+
+// ---------------------------------------------------------------------------
+// Combine backward: a token's products with its rows are summed inside one
+// block (WIDE) or one 16-lane group, without atomics: the order is fixed.
+template <class Row, bool ROWS, bool CODES, bool WIDE, int NT, int NTI>
+__global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
+    const typename Row::elem* __restrict__ dy, int64_t ld_dy, const typename Row::elem* __restrict__ yp,
+    int64_t ld_yp, const int* __restrict__ dst, const float* __restrict__ w, int tokens, int k, int m,
+    typename Row::elem* __restrict__ rows, int64_t ld_r, uint8_t* __restrict__ q, int64_t ld_q,
+    float* __restrict__ s, int64_t ld_s, float* __restrict__ dw, int cols) {
+  __shared__ float red[kWideThreads / 64][kJ];
+  int t, piece0;
+  place<WIDE>(WIDE ? 1 : 16, t, piece0);
+  if (!WIDE && t >= tokens) return;
+  const int step = WIDE ? (int)blockDim.x : 16;
+  const int64_t p0 = (int64_t)t * k;
+  for (int j0 = 0; j0 < k; j0 += kJ) {
+    int d[kJ];
+    float wj[kJ], acc[kJ];
+#pragma unroll
+    for (int u = 0; u < kJ; ++u) {
+      const int64_t at = p0 + min(j0 + u, k - 1);
+      d[u] = dst[at];
+      wj[u] = w[at];
+      acc[u] = 0.f;
+    }
+    auto body = [&](auto whole, int piece) {
+      constexpr bool kWhole = decltype(whole)::value;
+      const int c = piece >> 4, c0 = piece_col<Row>(piece);
+      const typename Row::Raw graw = load_piece<Row, kWhole, NTI>(dy + (int64_t)t * ld_dy, c0, cols);
+      typename Row::Raw raw[kJ];
+#pragma unroll
+      for (int u = 0; u < kJ; ++u)
+        if (j0 + u < k && row_ok(d[u], m))
+          raw[u] = load_piece<Row, kWhole, NTI>(yp + (int64_t)d[u] * ld_yp, c0, cols);
+      bool in[Row::kRuns];
+#pragma unroll
+      for (int i = 0; i < Row::kRuns; ++i) in[i] = c0 + 64 * i < cols;
+      float g[8];
+      Row::unpack(graw, g);
+#pragma unroll
+      for (int u = 0; u < kJ; ++u) {
+        if (j0 + u >= k) break;
+        const bool kept = d[u] >= 0;
+        const int r = kept ? d[u] : -1 - d[u];
         if (!row_ok(r, m)) continue;
         float v[8];
         if (kept) {
-          load_cols<Row>(yp + (int64_t)r * ld_yp, c0, cols, v);
+          Row::unpack(raw[u], v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[u] = __builtin_fmaf(g[e], v[e], acc[u]);
+          for (int i = 0; i < Row::kRuns; ++i) {
+            float part = acc[u];
+#pragma unroll
+            for (int e = i * Row::kLen; e < (i + 1) * Row::kLen; ++e) part = __builtin_fmaf(g[e], v[e], part);
+            acc[u] = in[i] ? part : acc[u];
+          }
         }
-        const float wj = w[p0 + j0 + u];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = kept ? g[e] * wj : 0.f;
-        const typename Row::Raw raw = Row::pack(v);
-        if (ROWS) store_cols<Row>(rows + (int64_t)r * ld_r, c0, cols, v);
+        for (int e = 0; e < 8; ++e) v[e] = kept ? g[e] * wj[u] : 0.f;
+        const typename Row::Raw out = Row::pack(v);
+        if (ROWS) store_piece<Row, kWhole, NT>(rows + (int64_t)r * ld_r, c0, cols, out);
         if (CODES) {
-          Row::unpack(raw, v);  // the codes are those of the rounded row
+          Row::unpack(out, v);  // the codes are those of the rounded row
           uint32_t a = 0;
 #pragma unroll
           for (int e = 0; e < 8; ++e) a = max(a, abs_bits(v[e]));
           a = row16_max_u32(a);
           float sc, inv;
           group_scale(__uint_as_float(a), sc, inv);
-          store_codes(q + (int64_t)r * ld_q, c0, cols,
-                      pack4_e4m3_grp(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                      pack4_e4m3_grp(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-          if (lig == 0) s[(int64_t)r * ld_s + c] = sc;
+          store_codes<Row, kWhole, NT>(q + (int64_t)r * ld_q, c0, cols,
+                                       pack4_e4m3_grp(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                                       pack4_e4m3_grp(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+          if ((piece & 15) == 0) s[(int64_t)r * ld_s + c] = sc;
         }
       }
+    };
+    for (int piece = piece0; (piece >> 4) * 128 < cols; piece += step) {
+      if (no_cut<Row>(piece_col<Row>(piece), cols)) body(std::true_type{}, piece); else body(std::false_type{}, piece);
     }
+    const int nj = min(kJ, k - j0);
 #pragma unroll
-    for (int u = 0; u < kJ; ++u)
+    for (int u = 0; u < kJ; ++u) acc[u] = row16_sum(acc[u]);
+    if (WIDE) {
+      const int lane = threadIdx.x & 63, waves = (int)blockDim.x >> 6;
 #pragma unroll
-      for (int o = 32; o > 0; o >>= 1) acc[u] += __shfl_xor(acc[u], o);
-    if ((tid & 63) == 0)
+      for (int u = 0; u < kJ; ++u) {
+        acc[u] += __shfl_xor(acc[u], 16);
+        acc[u] += __shfl_xor(acc[u], 32);
+      }
+      if (lane == 0)
 #pragma unroll
-      for (int u = 0; u < kJ; ++u) red[tid >> 6][u] = acc[u];
-    __syncthreads();
-    if (tid < nj) dw[p0 + j0 + tid] = (red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]);
-    __syncthreads();
+        for (int u = 0; u < kJ; ++u) red[threadIdx.x >> 6][u] = acc[u];
+      __syncthreads();
+      if ((int)threadIdx.x < nj) {
+        float sum = 0.f;
+        for (int i = 0; i < waves; ++i) sum += red[i][threadIdx.x];
+        dw[p0 + j0 + threadIdx.x] = sum;
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int u = 0; u < kJ; ++u)
+        if ((threadIdx.x & 15) == u && u < nj) dw[p0 + j0 + u] = acc[u];
+    }
   }
 }
+
+// Blocks of wide rows: the row's pieces in as few slices as blocks of
+// kWideThreads allow, of equal length up to a wave (7168 columns: two slices of
+// 448 threads, where slices of 512 would leave an eighth of the lanes idle).
+// The combine gradient of 32768 rows of 7168: 246 us so, 260 with blocks of
+// 128, 249 with 256 and 248 with 1024; the other kernels differ less.
+struct Shape {
+  bool wide;
+  int slices, threads;
+  int64_t pieces;  // of 8 columns, to whole 128-column groups
+};
+Shape shape_of(int64_t cols) {
+  Shape h;
+  h.wide = cols >= 512;
+  h.pieces = (cols + 127) / 128 * 16;
+  h.slices = h.wide ? (int)((h.pieces + kWideThreads - 1) / kWideThreads) : 1;
+  h.threads = h.wide ? (int)(((h.pieces + h.slices - 1) / h.slices + 63) / 64 * 64) : 256;
+  return h;
+}
+
+// Output runs that are aligned to their own size, in rows a multiple of that
+// apart, make whole segments, which are stored past the caches: the combine
+// gradient of 32768 rows of 7168 takes 246 us so and 271 us through them, the
+// dispatch to 16384 rows 69 and 81.  Cut segments lose by it (rows of 2047
+// BF16 columns: 21 us through the caches, 30 past them).
+bool aligned_out(const MoeRows& a) {
+  auto on = [](const void* p, int64_t row_bytes, int to) {
+    return !p || (reinterpret_cast<uintptr_t>(p) % to == 0 && row_bytes % to == 0);
+  };
+  return on(a.rows, a.ld_rows * (a.bf16 ? 2 : 4), 16) && on(a.q, a.ld_q, a.bf16 ? 8 : 4);
+}
+
+template <class F>
+void with_flag(bool v, F f) {
+  if (v) f(std::true_type{}); else f(std::false_type{});
+}
+template <class F>
+void with_row(bool bf16, F f) {
+  if (bf16) f(RowBF16{}); else f(RowF32{});
+}
+// The outputs asked for: rows, codes or both.
+template <class F>
+void with_outputs(const MoeRows& a, F f) {
+  if (a.rows && a.q) f(std::true_type{}, std::true_type{});
+  else if (a.q) f(std::false_type{}, std::true_type{});
+  else f(std::true_type{}, std::false_type{});
+}
+
+// Rows that cannot all stay in the 256 MiB cache in front of the memory are
+// read past the caches: combining 32768 rows of 7168 takes 94 us so and 102 us
+// through them.  Rows that may still be there lose by it (34 MB of rows, just
+// written: 16 us through the caches, 21 us past them).
+bool streamed(const MoeRows& a) { return a.tokens * a.k * a.cols * (a.bf16 ? 2 : 4) > ((int64_t)256 << 20); }
 
 }  // namespace
 
 hipError_t launch_moe_dispatch(const MoeRows& a, const void* x, int64_t ld_x, hipStream_t st) {
-  const int ngr = (int)((a.cols + 127) / 128);
-  const int total = (int)(a.tokens * ngr);
-  const dim3 grid((uint32_t)(((int64_t)total + 15) / 16));
-  auto go = [&](auto row, auto fr, auto fc) {
+  const Shape h = shape_of(a.cols);
+  const int per_token = h.wide ? h.slices : (int)h.pieces;
+  const uint32_t grid = (uint32_t)(h.wide ? a.tokens * h.slices : (a.tokens * h.pieces + 255) / 256);
+  with_row(a.bf16, [&](auto row) {
     typedef decltype(row) Row;
     typedef typename Row::elem E;
-    hipLaunchKernelGGL((k_dispatch<Row, decltype(fr)::value, decltype(fc)::value>), grid, dim3(256), 0, st,
-                       (const E*)x, ld_x, a.dst, (int)a.k, (int)(a.tokens * a.k), (E*)a.rows, a.ld_rows, a.q, a.ld_q,
-                       a.s, a.ld_s, (int)a.cols, ngr, total);
-  };
-  using T = std::true_type;
-  using F = std::false_type;
-  auto pick = [&](auto row) {
-    if (a.rows && a.q) go(row, T{}, T{});
-    else if (a.q) go(row, F{}, T{});
-    else go(row, T{}, F{});
-  };
-  if (a.bf16) pick(RowBF16{}); else pick(RowF32{});
+    with_outputs(a, [&](auto fr, auto fc) {
+      with_flag(h.wide, [&](auto wide) {
+        with_flag(aligned_out(a), [&](auto nt) {
+          hipLaunchKernelGGL((k_dispatch<Row, fr.value, fc.value, wide.value, nt.value>), dim3(grid),
+                             dim3(h.threads), 0, st, (const E*)x, ld_x, a.dst, (int)a.tokens, (int)a.k,
+                             (int)(a.tokens * a.k), (E*)a.rows, a.ld_rows, a.q, a.ld_q, a.s, a.ld_s, (int)a.cols,
+                             per_token);
+        });
+      });
+    });
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_moe_gather(const MoeRows& a, const float* w, void* y, int64_t ld_y, hipStream_t st) {
-  const int nch = (int)((a.cols + 7) / 8);
-  const int total = (int)(a.tokens * nch);
-  const dim3 grid((uint32_t)(((int64_t)total + 255) / 256));
-  auto go = [&](auto row, auto fw) {
+  const Shape h = shape_of(a.cols);
+  const int per_token = h.wide ? h.slices : (int)h.pieces;
+  const uint32_t grid = (uint32_t)(h.wide ? a.tokens * h.slices : (a.tokens * h.pieces + 255) / 256);
+  with_row(a.bf16, [&](auto row) {
     typedef decltype(row) Row;
     typedef typename Row::elem E;
-    hipLaunchKernelGGL((k_gather<Row, decltype(fw)::value>), grid, dim3(256), 0, st, (const E*)a.rows, a.ld_rows,
-                       a.dst, w, (int)a.k, (int)(a.tokens * a.k), (E*)y, ld_y, (int)a.cols, nch, total);
-  };
-  auto pick = [&](auto row) {
-    if (w) go(row, std::true_type{}); else go(row, std::false_type{});
-  };
-  if (a.bf16) pick(RowBF16{}); else pick(RowF32{});
+    with_flag(w != nullptr, [&](auto fw) {
+      with_flag(h.wide, [&](auto wide) {
+        with_flag(streamed(a), [&](auto nt) {
+          hipLaunchKernelGGL((k_gather<Row, fw.value, wide.value, nt.value>), dim3(grid), dim3(h.threads), 0, st,
+                             (const E*)a.rows, a.ld_rows, a.dst, w, (int)a.tokens, (int)a.k, (int)(a.tokens * a.k),
+                             (E*)y, ld_y, (int)a.cols, per_token);
+        });
+      });
+    });
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_bwd(const MoeRows& a, const void* dy, int64_t ld_dy, const void* yp, int64_t ld_yp,
                                   const float* w, float* dw, hipStream_t st) {
-  const int ngr = (int)((a.cols + 127) / 128);
-  const dim3 grid((uint32_t)a.tokens);
-  auto go = [&](auto row, auto fr, auto fc) {
+  const Shape h = shape_of(a.cols);
+  const uint32_t grid = (uint32_t)(h.wide ? a.tokens : (a.tokens + 15) / 16);
+  with_row(a.bf16, [&](auto row) {
     typedef decltype(row) Row;
     typedef typename Row::elem E;
-    hipLaunchKernelGGL((k_combine_bwd<Row, decltype(fr)::value, decltype(fc)::value>), grid, dim3(256), 0, st,
-                       (const E*)dy, ld_dy, (const E*)yp, ld_yp, a.dst, w, (int)a.k, (int)(a.tokens * a.k),
-                       (E*)a.rows, a.ld_rows, a.q, a.ld_q, a.s, a.ld_s, dw, (int)a.cols, ngr);
-  };
-  using T = std::true_type;
-  using F = std::false_type;
-  auto pick = [&](auto row) {
-    if (a.rows && a.q) go(row, T{}, T{});
-    else if (a.q) go(row, F{}, T{});
-    else go(row, T{}, F{});
-  };
-  if (a.bf16) pick(RowBF16{}); else pick(RowF32{});
+    with_outputs(a, [&](auto fr, auto fc) {
+      with_flag(h.wide, [&](auto wide) {
+        with_flag(aligned_out(a), [&](auto nt) {
+          with_flag(streamed(a), [&](auto nti) {
+            hipLaunchKernelGGL((k_combine_bwd<Row, fr.value, fc.value, wide.value, nt.value, nti.value>), dim3(grid),
+                               dim3(h.threads), 0, st, (const E*)dy, ld_dy, (const E*)yp, ld_yp, a.dst, w,
+                               (int)a.tokens, (int)a.k, (int)(a.tokens * a.k), (E*)a.rows, a.ld_rows, a.q, a.ld_q,
+                               a.s, a.ld_s, dw, (int)a.cols);
+          });
+        });
+      });
+    });
+  });
   return hipGetLastError();
 }
 

@@ -1,5 +1,5 @@
-// Row access shared by the MoE row kernels and gradient clipping: 8 elements
-// of a row as 16-byte accesses at ANY element alignment.  gfx950 global
+// Row access shared by the MoE row kernels and gradient clipping: elements of a
+// row as 16-byte accesses at ANY element alignment.  gfx950 global
 // memory instructions take multi-dword accesses at any byte address, so rows
 // whose length is odd use the same instructions as aligned ones; only the
 // alignment the compiler may assume differs.
@@ -11,6 +11,7 @@ namespace fp8q {
 
 typedef u32x4 u32x4_u __attribute__((aligned(1)));
 typedef u32x2 u32x2_u __attribute__((aligned(1)));
+typedef uint32_t u32_u __attribute__((aligned(1)));
 
 template <int NT>
 __device__ __forceinline__ u32x4 ld16u(const void* p) {
@@ -28,6 +29,12 @@ __device__ __forceinline__ void st8u(void* p, u32x2 v) {
   else *reinterpret_cast<u32x2_u*>(p) = v;
 }
 
+template <int NT>
+__device__ __forceinline__ void st4u(void* p, uint32_t v) {
+  if (NT) __builtin_nontemporal_store(v, reinterpret_cast<u32_u*>(p));
+  else *reinterpret_cast<u32_u*>(p) = v;
+}
+
 // Two FP32 values -> two BF16 values in one dword, round to nearest even (the
 // conversion instruction; a NaN stays a NaN).
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -36,93 +43,121 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
-// Row element types.  Raw is 8 elements as loaded; unpack widens them to
-// FP32, pack rounds them to the type.
+// Row element types.  A lane holds 8 columns of a 128-column group as runs of
+// 16 bytes: one of 8 BF16 columns, or two of 4 FP32 columns 64 apart, so that
+// 16 lanes always access a contiguous 256 bytes (FP32 pieces of 8 neighbouring
+// columns made every store instruction write half of each 32 bytes, which
+// halved the rate of stores past the caches).  Raw is the runs as loaded;
+// unpack widens them to FP32, pack rounds them to the type.
 struct RowBF16 {
   typedef uint16_t elem;
-  struct Raw { u32x4 a; };
-  template <int NT = 0>
-  __device__ __forceinline__ static Raw load8(const elem* p) { return Raw{ld16u<NT>(p)}; }
+  static constexpr int kRuns = 1, kLen = 8;
+  struct Raw { u32x4 a[kRuns]; };
   __device__ __forceinline__ static void unpack(const Raw& r, float v[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(r.a[i] << 16);
-      v[2 * i + 1] = __uint_as_float(r.a[i] & 0xFFFF0000u);
+      v[2 * i] = __uint_as_float(r.a[0][i] << 16);
+      v[2 * i + 1] = __uint_as_float(r.a[0][i] & 0xFFFF0000u);
     }
   }
   __device__ __forceinline__ static Raw pack(const float v[8]) {
     Raw r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.a[i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) r.a[0][i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
     return r;
   }
-  template <int NT = 0>
-  __device__ __forceinline__ static void store8(elem* p, const Raw& r) { st16u<NT>(p, r.a); }
   __device__ __forceinline__ static float load1(const elem* p) { return bf16_to_f32(*p); }
   __device__ __forceinline__ static void store1(elem* p, float v) { *p = (elem)pack2_bf16(v, 0.f); }
 };
 
 struct RowF32 {
   typedef float elem;
-  struct Raw { u32x4 a, b; };
-  template <int NT = 0>
-  __device__ __forceinline__ static Raw load8(const elem* p) { return Raw{ld16u<NT>(p), ld16u<NT>(p + 4)}; }
+  static constexpr int kRuns = 2, kLen = 4;
+  struct Raw { u32x4 a[kRuns]; };
   __device__ __forceinline__ static void unpack(const Raw& r, float v[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = __uint_as_float(r.a[i]);
-      v[4 + i] = __uint_as_float(r.b[i]);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.a[i >> 2][i & 3]);
   }
   __device__ __forceinline__ static Raw pack(const float v[8]) {
     Raw r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      r.a[i] = __float_as_uint(v[i]);
-      r.b[i] = __float_as_uint(v[4 + i]);
-    }
+    for (int i = 0; i < 8; ++i) r.a[i >> 2][i & 3] = __float_as_uint(v[i]);
     return r;
-  }
-  template <int NT = 0>
-  __device__ __forceinline__ static void store8(elem* p, const Raw& r) {
-    st16u<NT>(p, r.a);
-    st16u<NT>(p + 4, r.b);
   }
   __device__ __forceinline__ static float load1(const elem* p) { return *p; }
   __device__ __forceinline__ static void store1(elem* p, float v) { *p = v; }
 };
 
-// 8 elements from column c0 of a row of `cols`, zeros past its end.
-template <class Row, int NT = 0>
-__device__ __forceinline__ void load_cols(const typename Row::elem* p, int c0, int cols, float v[8]) {
-  if (c0 + 8 <= cols) {
-    Row::unpack(Row::template load8<NT>(p + c0), v);
-  } else {
+// True if no lane of the wave has a run that the row's end cuts: then its runs
+// are inside or outside as a whole.  The branch on it is uniform, so loads and
+// stores inside carry no masks of single columns.
+template <class Row>
+__device__ __forceinline__ bool no_cut(int c0, int cols) {
+  bool ok = true;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c0 + e < cols ? Row::load1(p + c0 + e) : 0.f;
+  for (int r = 0; r < Row::kRuns; ++r) {
+    const int cr = c0 + 64 * r;
+    ok = ok && (cr + Row::kLen <= cols || cr >= cols);
+  }
+  return __all(ok);
+}
+
+// A lane's runs from column c0, zeros past the row's end.  WHOLE: no_cut
+// holds; a run outside reads the row's last columns (of the same group), and
+// its lane drops it.
+template <class Row, bool WHOLE, int NT>
+__device__ __forceinline__ typename Row::Raw load_piece(const typename Row::elem* p, int c0, int cols) {
+  typename Row::Raw raw;
+#pragma unroll
+  for (int r = 0; r < Row::kRuns; ++r) {
+    const int cr = c0 + 64 * r;
+    if (WHOLE) {
+      raw.a[r] = ld16u<NT>(p + min(cr, cols - Row::kLen));
+    } else if (cr + Row::kLen <= cols) {
+      raw.a[r] = ld16u<NT>(p + cr);
+    } else {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = e < Row::kLen && cr + e < cols ? Row::load1(p + cr + e) : 0.f;
+      raw.a[r] = Row::pack(v).a[0];
+    }
+  }
+  return raw;
+}
+
+template <class Row, bool WHOLE, int NT>
+__device__ __forceinline__ void store_piece(typename Row::elem* p, int c0, int cols, const typename Row::Raw& raw) {
+  float v[8];
+  if (!WHOLE) Row::unpack(raw, v);
+#pragma unroll
+  for (int r = 0; r < Row::kRuns; ++r) {
+    const int cr = c0 + 64 * r;
+    if (WHOLE ? cr < cols : cr + Row::kLen <= cols) {
+      st16u<NT>(p + cr, raw.a[r]);
+    } else if (!WHOLE) {
+#pragma unroll
+      for (int e = 0; e < Row::kLen; ++e)
+        if (cr + e < cols) Row::store1(p + cr + e, v[r * Row::kLen + e]);
+    }
   }
 }
 
-template <class Row, int NT = 0>
-__device__ __forceinline__ void store_cols(typename Row::elem* p, int c0, int cols, const float v[8]) {
-  if (c0 + 8 <= cols) {
-    Row::template store8<NT>(p + c0, Row::pack(v));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c0 + e < cols) Row::store1(p + c0 + e, v[e]);
-  }
-}
-
-// 8 codes (two dwords) to column c0 of a code row of `cols`.
-template <int NT = 0>
+// The codes of a lane's 8 columns (two dwords) to a code row.
+template <class Row, bool WHOLE, int NT>
 __device__ __forceinline__ void store_codes(uint8_t* p, int c0, int cols, uint32_t w0, uint32_t w1) {
-  if (c0 + 8 <= cols) {
-    st8u<NT>(p + c0, u32x2{w0, w1});
-  } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c0 + e < cols) p[c0 + e] = (uint8_t)(((e < 4 ? w0 : w1) >> (8 * (e & 3))) & 0xFF);
+  for (int r = 0; r < Row::kRuns; ++r) {
+    const int cr = c0 + 64 * r;
+    if (WHOLE ? cr < cols : cr + Row::kLen <= cols) {
+      if (Row::kRuns == 1) st8u<NT>(p + cr, u32x2{w0, w1});
+      else st4u<NT>(p + cr, r == 0 ? w0 : w1);
+    } else if (!WHOLE) {
+#pragma unroll
+      for (int i = 0; i < Row::kLen; ++i) {
+        const int e = r * Row::kLen + i;
+        if (cr + i < cols) p[cr + i] = (uint8_t)(((e < 4 ? w0 : w1) >> (8 * (e & 3))) & 0xFF);
+      }
+    }
   }
 }
 
