@@ -40,7 +40,6 @@ moe_dispatch, moe_dispatch_quant, moe_dispatch_bwd, moe_combine,
 moe_combine_bwd, moe_combine_bwd_quant, grad_clip.
 """
 
-import array
 import contextlib
 import ctypes
 import os
@@ -52,6 +51,7 @@ LIB_PATH = os.path.join(_HERE, "libfp8q.so")
 # the same library built with FP8Q_DEBUG: its grouped entry points also read
 # the device expert offsets back and reject malformed ones (synchronously)
 DEBUG_LIB_PATH = os.path.join(_HERE, "libfp8q_debug.so")
+CALLS_PATH = os.path.join(_HERE, "_calls.so")
 
 FP8Q_BF16, FP8Q_F32 = 0, 1
 _STATUS = ["FP8Q_OK", "FP8Q_ERR_NULL", "FP8Q_ERR_SHAPE", "FP8Q_ERR_STRIDE",
@@ -173,9 +173,14 @@ def set_gemm_tile(tile):
 
 
 # ----------------------------------------------------------------- marshalling
+# torch's current stream as a pointer: 0.2 us, where building the Stream object
+# of torch.cuda.current_stream() took 2.8 us of every call
+_current_device, _current_stream = torch.cuda.current_device, getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -757,7 +762,6 @@ def grouped_gemm_mx_dgrad(dyq, dys, wq_t, ws_t, offsets, out_dtype=torch.bfloat1
 # ----------------------------------------------------------------- MoE routing
 MAX_EXPERTS, MAX_TOP_K = 1024, 32
 SCORES = {"softmax": 0, "sigmoid": 1}
-_I32 = torch.int32
 
 
 def _score(score):
@@ -766,49 +770,61 @@ def _score(score):
     return SCORES[score]
 
 
-def _map(t, what, tokens=None):
-    """A [T, k] int32 map or id tensor; returns its shape."""
-    if t.dim() != 2 or (tokens is not None and t.shape[0] != tokens):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [{'T' if tokens is None else tokens}, k]")
-    if t.dtype != _I32:
-        raise TypeError(f"{what}: dtype {t.dtype}, expected {_I32}")
-    return t.shape
+_bound = None
 
 
-def _dense(*ts):
-    for t in ts:
-        if t is not None and not t.is_contiguous():
-            raise ValueError("ids, maps, weights, offsets, biases, workspaces and gradients must be contiguous")
+def _native():
+    """The native calls of these operators (csrc/calls.cpp), bound to the
+    library once."""
+    global _bound
+    if _bound is None:
+        _bound = _bind(load_library())
+    return _bound
+
+
+def _bind(lib):
+    if not os.path.exists(CALLS_PATH):
+        raise RuntimeError(f"{os.path.basename(CALLS_PATH)} not built ({CALLS_PATH}); run __graft_entry__.build()")
+    from . import _calls
+    names = [n for n in EXPORTS if n.startswith(("fp8q_moe_", "fp8q_grad_"))]
+    _calls.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _current_device,
+                _current_stream, _check)
+    return _calls
+
+
+def _handle(stream):
+    return None if stream is None else _stream(stream)
+
+
+def _on(stream, call, *args):
+    """call(*args, stream's handle), which allocates on the stream it runs on,
+    so that the caching allocator hands memory freed at the call's end only to
+    later work of that stream."""
+    if stream is None:
+        return call(*args, None)
+    handle = _stream(stream)
+    side = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle)
+    with torch.cuda.stream(side):
+        return call(*args, handle)
+
+
+def _required(**outputs):
+    for name, t in outputs.items():
+        if t is None:
+            raise ValueError(f"{name} is required")
 
 
 def fp8q_moe_route(logits, ids, weights, score="softmax", bias=None, renormalize=True, scale=1.0, stream=None):
     """The k = ids.shape[1] best experts of every token: ids [T, k] int32,
     weights [T, k] FP32 from logits [T, E] (BF16 or FP32)."""
-    tokens, experts = logits.shape
-    k = _map(ids, "ids", tokens)[1]
-    _expect(weights, (tokens, k), _F32, "weights")
-    if bias is not None:
-        _expect(bias, (experts,), _F32, "bias")
-    _on_gpu(logits, ids, weights, bias)
-    _dense(ids, weights, bias)
-    _check(load_library().fp8q_moe_route(_ptr(logits), _dtype_code(logits), tokens, experts, _ld(logits), k,
-                                         _score(score), _ptr(bias), int(bool(renormalize)), scale, _ptr(ids),
-                                         _ptr(weights), _stream(stream)),
-           "fp8q_moe_route")
+    _required(ids=ids, weights=weights)
+    _native().moe_route(logits, 0, _score(score), bias, bool(renormalize), scale, ids, weights, _handle(stream))
 
 
 def fp8q_moe_route_bwd(dweights, logits, ids, dlogits, score="softmax", renormalize=True, scale=1.0, stream=None):
     """Gradient of the weights to the logits, dlogits [T, E] of the logits' type."""
-    tokens, experts = logits.shape
-    k = _map(ids, "ids", tokens)[1]
-    _expect(dweights, (tokens, k), _F32, "dweights")
-    _expect(dlogits, (tokens, experts), logits.dtype, "dlogits")
-    _on_gpu(dweights, logits, ids, dlogits)
-    _dense(dweights, ids)
-    _check(load_library().fp8q_moe_route_bwd(_ptr(dweights), _ptr(logits), _dtype_code(logits), tokens, experts,
-                                             _ld(logits), _ptr(ids), k, _score(score), int(bool(renormalize)), scale,
-                                             _ptr(dlogits), _ld(dlogits), _stream(stream)),
-           "fp8q_moe_route_bwd")
+    _required(dlogits=dlogits)
+    _native().moe_route_bwd(dweights, logits, ids, _score(score), bool(renormalize), scale, dlogits, _handle(stream))
 
 
 def moe_sort_workspace(pairs, experts):
@@ -823,89 +839,33 @@ def fp8q_moe_sort(ids, experts, offsets, dst, src=None, workspace=None, cover=Fa
     """Rows in expert order: offsets [experts + 1], dst [T, k] (row of each
     pair, or -1 - row for a dropped one), src [T*k] the pair of each row.
     workspace: moe_sort_workspace(T*k, experts) bytes (uint8), None if 0."""
-    tokens, k = _map(ids, "ids")
-    _expect(offsets, (experts + 1,), _I32, "offsets")
-    _expect(dst, (tokens, k), _I32, "dst")
-    if src is not None:
-        _expect(src, (tokens * k,), _I32, "src")
-    if workspace is not None:
-        _expect(workspace, (None,), _U8, "workspace")
-    _on_gpu(ids, offsets, dst, src, workspace)
-    _dense(ids, offsets, dst, src, workspace)
-    _check(load_library().fp8q_moe_sort(_ptr(ids), tokens * k, experts, int(bool(cover)), _ptr(offsets), _ptr(dst),
-                                        _ptr(src), _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                        _stream(stream)),
-           "fp8q_moe_sort")
-
-
-def _expect_rows(rows, q, scale, m, cols, dtype):
-    if rows is not None:
-        _expect(rows, (m, cols), dtype, "rows")
-    if q is not None or scale is not None:
-        _expect(q, (m, cols), _U8, "q")
-        _expect(scale, (m, _cdiv(cols, 128)), _F32, "scale")
-
-
-def _row_args(rows, q, scale):
-    return (_ptr(rows), _ld(rows) if rows is not None else 0, _ptr(q), _ld(q) if q is not None else 0, _ptr(scale),
-            _ld(scale) if scale is not None else 0)
+    _required(offsets=offsets, dst=dst)
+    _native().moe_sort(ids, experts, bool(cover), offsets, dst, src, workspace, _handle(stream))
 
 
 def fp8q_moe_dispatch(x, dst, rows=None, q=None, scale=None, stream=None):
     """Token rows x [T, H] into expert order: rows [T*k, H] and/or their 1x128
     codes and scales; zeros for dropped pairs."""
-    tokens, cols = x.shape
-    k = _map(dst, "dst", tokens)[1]
-    _expect_rows(rows, q, scale, tokens * k, cols, x.dtype)
-    _on_gpu(x, dst, rows, q, scale)
-    _dense(dst)
-    _check(load_library().fp8q_moe_dispatch(_ptr(x), _dtype_code(x), tokens, cols, _ld(x), _ptr(dst), k,
-                                            *_row_args(rows, q, scale), _stream(stream)),
-           "fp8q_moe_dispatch")
+    _native().moe_dispatch(x, dst, rows, q, scale, 0, _handle(stream))
 
 
 def fp8q_moe_dispatch_bwd(drows, dst, dx, stream=None):
     """dx [T, H] = sum of each token's kept rows of drows [T*k, H]."""
-    tokens, k = _map(dst, "dst")
-    cols = drows.shape[1]
-    _expect(drows, (tokens * k, cols), drows.dtype, "drows")
-    _expect(dx, (tokens, cols), drows.dtype, "dx")
-    _on_gpu(drows, dst, dx)
-    _dense(dst)
-    _check(load_library().fp8q_moe_dispatch_bwd(_ptr(drows), _dtype_code(drows), tokens, cols, _ld(drows), _ptr(dst),
-                                                k, _ptr(dx), _ld(dx), _stream(stream)),
-           "fp8q_moe_dispatch_bwd")
+    _required(dx=dx)
+    _native().moe_dispatch_bwd(drows, dst, dx, _handle(stream))
 
 
 def fp8q_moe_combine(yp, dst, weights, y, stream=None):
     """y [T, H] = weighted sum of each token's kept rows of yp [T*k, H]."""
-    tokens, k = _map(dst, "dst")
-    cols = yp.shape[1]
-    _expect(yp, (tokens * k, cols), yp.dtype, "yp")
-    _expect(weights, (tokens, k), _F32, "weights")
-    _expect(y, (tokens, cols), yp.dtype, "y")
-    _on_gpu(yp, dst, weights, y)
-    _dense(dst, weights)
-    _check(load_library().fp8q_moe_combine(_ptr(yp), _dtype_code(yp), tokens, cols, _ld(yp), _ptr(dst), k,
-                                           _ptr(weights), _ptr(y), _ld(y), _stream(stream)),
-           "fp8q_moe_combine")
+    _required(y=y)
+    _native().moe_combine(yp, dst, weights, y, _handle(stream))
 
 
 def fp8q_moe_combine_bwd(dy, yp, dst, weights, dweights, rows=None, q=None, scale=None, stream=None):
     """Gradients of the combination: rows [T*k, H] (to yp) and/or their codes
     and scales, dweights [T, k]."""
-    tokens, cols = dy.shape
-    k = _map(dst, "dst", tokens)[1]
-    _expect(yp, (tokens * k, cols), dy.dtype, "yp")
-    _expect(weights, (tokens, k), _F32, "weights")
-    _expect(dweights, (tokens, k), _F32, "dweights")
-    _expect_rows(rows, q, scale, tokens * k, cols, dy.dtype)
-    _on_gpu(dy, yp, dst, weights, dweights, rows, q, scale)
-    _dense(dst, weights, dweights)
-    _check(load_library().fp8q_moe_combine_bwd(_ptr(dy), _ptr(yp), _dtype_code(dy), tokens, cols, _ld(dy), _ld(yp),
-                                               _ptr(dst), k, _ptr(weights), *_row_args(rows, q, scale),
-                                               _ptr(dweights), _stream(stream)),
-           "fp8q_moe_combine_bwd")
+    _required(dweights=dweights)
+    _native().moe_combine_bwd(dy, yp, dst, weights, dweights, rows, q, scale, 0, _handle(stream))
 
 
 def grad_clip_workspace(n):
@@ -918,130 +878,62 @@ def fp8q_grad_clip(grads, out, max_norm, norm, workspace, stream=None):
     clipping), out[i] = grads[i] * min(1, max_norm / norm), all FP32 or all
     BF16, grads[i] itself for clipping in place.
     workspace: grad_clip_workspace(len(grads)) bytes (uint8)."""
-    if len(out) != len(grads):
-        raise ValueError(f"out: {len(out)} tensors for {len(grads)} gradients")
-    ot = out[0].dtype if out else _F32
-    table = []
-    for g, o in zip(grads, out):
-        if g.dtype != _F32 or o.dtype != ot:
-            raise TypeError(f"gradients of {g.dtype} to {o.dtype}, expected {_F32} to {ot}")
-        if g.shape != o.shape:
-            raise ValueError(f"out: shape {tuple(o.shape)} for a gradient of {tuple(g.shape)}")
-        if not (g.is_contiguous() and o.is_contiguous()):
-            raise ValueError("gradients and their outputs must be contiguous")
-        table += (g.data_ptr(), o.data_ptr(), g.numel())
-    _expect(norm, (), _F32, "norm")
-    _expect(workspace, (None,), _U8, "workspace")
-    _on_gpu(norm, workspace, *grads, *out)
-    _dense(workspace)
-    arr = array.array("q", table)
-    _check(load_library().fp8q_grad_clip(arr.buffer_info()[0], len(grads), _dtype_code(out[0]) if out else FP8Q_F32,
-                                         max_norm, _ptr(workspace), workspace.numel(), _ptr(norm), _stream(stream)),
-           "fp8q_grad_clip")
-
-
-def _alloc_on(stream):
-    """Allocate on the stream the call runs on, so that the caching allocator
-    hands memory freed at the call's end only to later work of that stream."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
+    _required(norm=norm, workspace=workspace)
+    _native().grad_clip(grads, out, max_norm, norm, workspace, _handle(stream))
 
 
 def moe_route(logits, k, score="softmax", bias=None, renormalize=True, scale=1.0, stream=None):
     """The k best experts of every token and their weights: (ids, weights)."""
-    tokens = logits.shape[0]
-    with _alloc_on(stream):
-        ids = torch.empty((tokens, k), dtype=_I32, device=logits.device)
-        weights = torch.empty((tokens, k), dtype=_F32, device=logits.device)
-    fp8q_moe_route(logits, ids, weights, score, bias, renormalize, scale, stream)
-    return ids, weights
+    return _on(stream, _native().moe_route, logits, k, _score(score), bias, bool(renormalize), scale, None, None)
 
 
 def moe_route_bwd(dweights, logits, ids, score="softmax", renormalize=True, scale=1.0, stream=None):
     """Gradient of moe_route's weights to the logits, for the ids it chose."""
-    with _alloc_on(stream):
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    fp8q_moe_route_bwd(dweights, logits, ids, dlogits, score, renormalize, scale, stream)
-    return dlogits
+    return _on(stream, _native().moe_route_bwd, dweights, logits, ids, _score(score), bool(renormalize), scale, None)
 
 
 def moe_sort(ids, experts, cover=False, stream=None):
     """The pairs of ids [T, k] in expert order: (offsets, dst, src).  cover:
     dropped pairs' rows (zeros) count as the last expert's, as the grouped
     products' offsets need it where pairs are dropped."""
-    tokens, k = _map(ids, "ids")
-    need = moe_sort_workspace(tokens * k, experts)
-    with _alloc_on(stream):
-        offsets = torch.empty((experts + 1,), dtype=_I32, device=ids.device)
-        dst = torch.empty((tokens, k), dtype=_I32, device=ids.device)
-        src = torch.empty((tokens * k,), dtype=_I32, device=ids.device)
-        ws = torch.empty((need,), dtype=_U8, device=ids.device) if need else None
-    fp8q_moe_sort(ids, experts, offsets, dst, src, ws, cover, stream)
-    return offsets, dst, src
+    return _on(stream, _native().moe_sort, ids, experts, bool(cover), None, None, None, None)
 
 
-def _code_rows(m, cols, device):
-    """Code rows [m, cols] 16 bytes apart or a multiple of it, and their scales."""
-    q = torch.empty((m, _cdiv(cols, 16) * 16), dtype=_U8, device=device)
-    return q if q.shape[1] == cols else q[:, :cols], torch.empty((m, _cdiv(cols, 128)), dtype=_F32, device=device)
+_ROWS, _CODES = 1, 2
 
 
 def moe_dispatch(x, dst, stream=None):
     """Token rows into expert order (zeros for dropped pairs)."""
-    with _alloc_on(stream):
-        rows = torch.empty((dst.numel(), x.shape[1]), dtype=x.dtype, device=x.device)
-    fp8q_moe_dispatch(x, dst, rows, stream=stream)
-    return rows
+    return _on(stream, _native().moe_dispatch, x, dst, None, None, None, _ROWS)[0]
 
 
 def moe_dispatch_quant(x, dst, with_output=True, stream=None):
     """Dispatch with the 1x128 quantization of the rows: (rows or None, q, scale)."""
-    m, cols = dst.numel(), x.shape[1]
-    with _alloc_on(stream):
-        rows = torch.empty((m, cols), dtype=x.dtype, device=x.device) if with_output else None
-        q, scale = _code_rows(m, cols, x.device)
-    fp8q_moe_dispatch(x, dst, rows, q, scale, stream)
-    return rows, q, scale
+    want = _ROWS | _CODES if with_output else _CODES
+    return _on(stream, _native().moe_dispatch, x, dst, None, None, None, want)
 
 
 def moe_dispatch_bwd(drows, dst, stream=None):
     """Gradient of moe_dispatch: the sum of each token's kept rows."""
-    with _alloc_on(stream):
-        dx = torch.empty((dst.shape[0], drows.shape[1]), dtype=drows.dtype, device=drows.device)
-    fp8q_moe_dispatch_bwd(drows, dst, dx, stream)
-    return dx
+    return _on(stream, _native().moe_dispatch_bwd, drows, dst, None)
 
 
 def moe_combine(yp, dst, weights, stream=None):
     """Expert rows back into token order with the weights applied."""
-    with _alloc_on(stream):
-        y = torch.empty((dst.shape[0], yp.shape[1]), dtype=yp.dtype, device=yp.device)
-    fp8q_moe_combine(yp, dst, weights, y, stream)
-    return y
+    return _on(stream, _native().moe_combine, yp, dst, weights, None)
 
 
 def moe_combine_bwd(dy, yp, dst, weights, stream=None):
     """Gradients of moe_combine: (rows, dweights)."""
-    with _alloc_on(stream):
-        rows = torch.empty(yp.shape, dtype=dy.dtype, device=dy.device)
-        dweights = torch.empty(dst.shape, dtype=_F32, device=dy.device)
-    fp8q_moe_combine_bwd(dy, yp, dst, weights, dweights, rows, stream=stream)
-    return rows, dweights
+    out = _on(stream, _native().moe_combine_bwd, dy, yp, dst, weights, None, None, None, None, _ROWS)
+    return out[0], out[3]
 
 
 def moe_combine_bwd_quant(dy, yp, dst, weights, with_output=True, stream=None):
     """Gradients of moe_combine, those to the expert rows also (or only) as
     1x128 codes: (rows or None, q, scale, dweights)."""
-    m, cols = yp.shape
-    with _alloc_on(stream):
-        rows = torch.empty((m, cols), dtype=dy.dtype, device=dy.device) if with_output else None
-        q, scale = _code_rows(m, cols, dy.device)
-        dweights = torch.empty(dst.shape, dtype=_F32, device=dy.device)
-    fp8q_moe_combine_bwd(dy, yp, dst, weights, dweights, rows, q, scale, stream)
-    return rows, q, scale, dweights
+    want = _ROWS | _CODES if with_output else _CODES
+    return _on(stream, _native().moe_combine_bwd, dy, yp, dst, weights, None, None, None, None, want)
 
 
 # ----------------------------------------------------------- gradient clipping
@@ -1049,10 +941,4 @@ def grad_clip(grads, max_norm, out=None, stream=None):
     """Clips the FP32 gradients by their global norm into `out` (FP32 or BF16
     tensors of their shapes; None: in place).  Returns the norm before
     clipping, a 0-dim tensor on the GPU."""
-    out = grads if out is None else out
-    device = grads[0].device if grads else torch.device("cuda")
-    with _alloc_on(stream):
-        norm = torch.empty((), dtype=_F32, device=device)
-        ws = torch.empty((grad_clip_workspace(len(grads)),), dtype=_U8, device=device)
-    fp8q_grad_clip(grads, out, max_norm, norm, ws, stream)
-    return norm
+    return _on(stream, _native().grad_clip, grads, grads if out is None else out, max_norm, None, None)

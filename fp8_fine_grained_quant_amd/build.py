@@ -12,12 +12,15 @@ unroll the source asks for does not happen (either one turned a quantizer's
 warning).  libfp8q_debug.so links the same kernel
 objects with api.cpp compiled under FP8Q_DEBUG, whose grouped entry points
 also copy the device expert offsets to the host and reject malformed ones
-(a synchronous check the product library never makes).
+(a synchronous check the product library never makes).  _calls.so is host code
+only: the Python calls of the MoE routing operators, built against torch's
+headers; it finds the library's entry points when it is bound to them.
 """
 
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -26,10 +29,12 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8q.so")
 LIB_DEBUG = os.path.join(HERE, "libfp8q_debug.so")
+CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ["quant_kernels.hip", "quant_mx.hip", "gemm_fp8.hip", "gemm_mx.hip", "moe_route.hip", "moe_sort.hip", "moe_rows.hip",
            "grad_clip.hip", "api.cpp"]
 ARCH = os.environ.get("FP8Q_ARCH", "gfx950")
 
+ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -56,7 +61,7 @@ def _run(cmd, verbose):
     res = subprocess.run(cmd, capture_output=True, text=True)
     err = "\n".join(l for l in res.stderr.splitlines() if _NOISE not in l)
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{err}")
     return err
 
 
@@ -90,6 +95,23 @@ def _compile(src, obj, extra, verbose):
     return obj
 
 
+def _build_calls(verbose):
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = CALLS + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-D__HIP_PLATFORM_AMD__",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(ROCM, "include"),
+           "-isystem", sysconfig.get_path("include")]
+    for d in include_paths():
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "calls.cpp"), "-o", tmp]
+    for d in library_paths():
+        cmd += ["-L" + d]
+    _run(cmd + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"], verbose)
+    os.replace(tmp, CALLS)
+
+
 def _link(objs, out, verbose):
     tmp = out + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}"] + objs + ["-o", tmp], verbose)
@@ -100,8 +122,10 @@ def build(verbose=False):
     os.makedirs(OBJ, exist_ok=True)
     jobs = [(s, os.path.join(OBJ, os.path.splitext(s)[0] + ".o"), []) for s in SOURCES]
     jobs.append(("api.cpp", os.path.join(OBJ, "api_debug.o"), ["-DFP8Q_DEBUG"]))
-    with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 1)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 1)) as ex:
+        calls = ex.submit(_build_calls, verbose)
         objs = list(ex.map(lambda j: _compile(j[0], j[1], j[2], verbose), jobs))
+        calls.result()
     kernels, api, api_debug = objs[:-2], objs[-2], objs[-1]
     _link(kernels + [api], LIB, verbose)
     _link(kernels + [api_debug], LIB_DEBUG, verbose)

@@ -1,0 +1,93 @@
+"""What the native calls of the routing operators refuse before any work: wrong
+kinds of objects, missing outputs, sizes out of range (CPU tensors: nothing
+reaches a device)."""
+
+import subprocess
+import sys
+
+import pytest
+import torch
+
+import fp8_fine_grained_quant_amd as fq
+
+u8, f32, bf16, i32, i64 = torch.uint8, torch.float32, torch.bfloat16, torch.int32, torch.int64
+
+
+def z(*shape, dt=f32):
+    return torch.zeros(shape, dtype=dt)
+
+
+def refused(error, text, fn):
+    with pytest.raises(error) as e:
+        fn()
+    assert text in str(e.value), str(e.value)
+
+
+X, IDS, W = z(6, 32), z(6, 4, dt=i32), z(6, 4)
+
+
+def test_not_tensors():
+    refused(TypeError, "logits: expected a tensor", lambda: fq.moe_route([[1.0, 2.0]], 1))
+    refused(ValueError, "logits is required", lambda: fq.moe_route(None, 1))
+    refused(TypeError, "bias: expected a tensor", lambda: fq.moe_route(X, 2, bias=3.0))
+    refused(TypeError, "integer", lambda: fq.moe_route(X, "2"))
+    refused(ValueError, "relu", lambda: fq.moe_route(X, 2, score="relu"))
+    refused(TypeError, "dst: expected a tensor", lambda: fq.moe_dispatch(X, [0, 1]))
+    refused(ValueError, "weights is required", lambda: fq.moe_combine(z(24, 8), IDS, None))
+    refused(TypeError, "out: expected a tensor", lambda: fq.grad_clip([z(3)], 1.0, out=[1]))
+    refused(TypeError, "sequence", lambda: fq.grad_clip(5, 1.0))
+    refused(TypeError, "arguments", lambda: fq._native().moe_combine(X))
+
+
+def test_missing_outputs():
+    refused(ValueError, "ids is required", lambda: fq.fp8q_moe_route(X, None, W))
+    refused(ValueError, "weights is required", lambda: fq.fp8q_moe_route(X, IDS, None))
+    refused(ValueError, "dlogits is required", lambda: fq.fp8q_moe_route_bwd(W, X, IDS, None))
+    refused(ValueError, "offsets is required", lambda: fq.fp8q_moe_sort(IDS, 8, None, IDS))
+    refused(ValueError, "dst is required", lambda: fq.fp8q_moe_sort(IDS, 8, z(9, dt=i32), None))
+    refused(ValueError, "dx is required", lambda: fq.fp8q_moe_dispatch_bwd(z(24, 8), IDS, None))
+    refused(ValueError, "y is required", lambda: fq.fp8q_moe_combine(z(24, 8), IDS, W, None))
+    refused(ValueError, "dweights is required", lambda: fq.fp8q_moe_combine_bwd(z(6, 8), z(24, 8), IDS, W, None))
+    refused(ValueError, "norm is required", lambda: fq.fp8q_grad_clip([], [], 1.0, None, z(8, dt=u8)))
+    refused(ValueError, "q is required", lambda: fq.fp8q_moe_dispatch(X, IDS, scale=z(24, 1)))
+
+
+def test_shapes_and_types():
+    refused(ValueError, "2-D", lambda: fq.moe_route(z(6), 2))
+    refused(ValueError, "2-D", lambda: fq.moe_combine(z(24), IDS, W))
+    refused(TypeError, "torch.int64", lambda: fq.moe_sort(z(6, 4, dt=i64), 8))
+    refused(TypeError, "torch.float32", lambda: fq.moe_sort(W, 8))
+    refused(ValueError, "GPU tensors only", lambda: fq.moe_sort(IDS, 8))
+    refused(ValueError, "GPU tensors only", lambda: fq.moe_route(X, 2))
+    refused(ValueError, "GPU tensors only", lambda: fq.grad_clip([z(3)], 1.0))
+    refused(ValueError, "weights", lambda: fq.moe_combine(z(24, 8), IDS, z(6, 3)))
+    refused(TypeError, "weights", lambda: fq.moe_combine(z(24, 8), IDS, z(6, 4, dt=bf16)))
+    refused(ValueError, "yp: shape (24, 7), expected (24, 8)", lambda: fq.moe_combine_bwd(z(6, 8), z(24, 7), IDS, W))
+    refused(TypeError, "yp: dtype torch.bfloat16", lambda: fq.moe_combine_bwd(z(6, 8), z(24, 8, dt=bf16), IDS, W))
+
+
+@pytest.mark.gpu
+def test_refusals_on_the_gpu():
+    d = lambda t: t.cuda()
+    shape = "FP8Q_ERR_SHAPE"
+    for k in (0, -1, 33, 1 << 40):
+        refused(fq.Fp8qError, shape, lambda: fq.moe_route(d(z(6, 64)), k))
+    refused(fq.Fp8qError, shape, lambda: fq.moe_route(d(X), 2, scale=float("nan")))
+    refused(fq.Fp8qError, "FP8Q_ERR_STRIDE", lambda: fq.moe_route(d(z(1, 32)).expand(6, 32), 2))
+    refused(ValueError, "contiguous rows", lambda: fq.moe_route(d(z(32, 6)).t(), 2))
+    refused(TypeError, "unsupported dtype torch.float16", lambda: fq.moe_route(d(X).half(), 2))
+    refused(ValueError, "must be contiguous", lambda: fq.moe_dispatch(d(X), d(z(4, 6, dt=i32)).t()))
+    refused(ValueError, "24 pairs, 2000 experts", lambda: fq.moe_sort(d(IDS), 2000))
+    refused(fq.Fp8qError, "FP8Q_ERR_NULL", lambda: fq.fp8q_moe_dispatch(d(X), d(IDS)))
+    refused(fq.Fp8qError, shape, lambda: fq.grad_clip([d(z(3))], -1.0))
+    refused(TypeError, "torch.float16", lambda: fq.grad_clip([d(z(3))], 1.0, out=[d(z(3)).half()]))
+    refused(ValueError, "GPU tensors only", lambda: fq.grad_clip([d(z(3)), z(3)], 1.0))
+
+
+def test_missing_build_is_named(tmp_path):
+    """Without the built module the calls fail by name; there is no slower path."""
+    code = ("import fp8_fine_grained_quant_amd as fq, torch\n"
+            f"fq.CALLS_PATH = {str(tmp_path / '_calls.so')!r}\n"
+            "try:\n    fq.moe_sort(torch.zeros(2, 2, dtype=torch.int32), 4)\n"
+            "except RuntimeError as e:\n    assert 'not built' in str(e), e\nelse:\n    raise SystemExit(1)\n")
+    assert subprocess.run([sys.executable, "-c", code]).returncode == 0
