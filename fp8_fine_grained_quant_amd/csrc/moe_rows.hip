@@ -24,6 +24,16 @@ constexpr int kJ = 8;              // choices handled together: 8 row loads in f
 constexpr int kWideThreads = 512;  // most threads of a block that works on one token
 
 __device__ __forceinline__ bool row_ok(int r, int m) { return (uint32_t)r < (uint32_t)m; }
+// The row of a map entry, kept or dropped.
+__device__ __forceinline__ int row_of(int d) { return d >= 0 ? d : -1 - d; }
+
+template <class F>
+__device__ __forceinline__ void each_choice(F f) {
+  f(std::integral_constant<int, 0>{}); f(std::integral_constant<int, 1>{});
+  f(std::integral_constant<int, 2>{}); f(std::integral_constant<int, 3>{});
+  f(std::integral_constant<int, 4>{}); f(std::integral_constant<int, 5>{});
+  f(std::integral_constant<int, 6>{}); f(std::integral_constant<int, 7>{});
+}
 
 // 16 lanes handle a 128-column group of a row, 8 columns each.  WIDE rows (a
 // wave's 512 columns or more) give a block to one token, or to a slice of its
@@ -68,14 +78,9 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_dispatch(
     if (CODES) {
       // a run outside holds values of its own group's last columns: they do not
       // change the group's max-abs
-      float v[8];
+      float v[8], inv;
       Row::unpack(raw, v);
-      uint32_t a = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a = max(a, abs_bits(v[e]));
-      a = row16_max_u32(a);
-      float inv;
-      group_scale(__uint_as_float(a), sc, inv);
+      group_scale(__uint_as_float(row16_max_u32(Row::max_bits(raw))), sc, inv);
       w0 = pack4_e4m3_grp(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
       w1 = pack4_e4m3_grp(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
     }
@@ -87,7 +92,7 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_dispatch(
       for (int u = 0; u < kJ; ++u) {
         if (j0 + u >= k) break;
         const bool kept = dj[u] >= 0;
-        const int r = kept ? dj[u] : -1 - dj[u];
+        const int r = row_of(dj[u]);
         if (!row_ok(r, m)) continue;
         if (ROWS) {
           typename Row::Raw z{};
@@ -164,15 +169,18 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
   const int step = WIDE ? (int)blockDim.x : 16;
   const int64_t p0 = (int64_t)t * k;
   for (int j0 = 0; j0 < k; j0 += kJ) {
-    int d[kJ];
+    int d[kJ], r[kJ];  // a choice's map entry and row; m: no choice
     float wj[kJ], acc[kJ];
 #pragma unroll
     for (int u = 0; u < kJ; ++u) {
       const int64_t at = p0 + min(j0 + u, k - 1);
       d[u] = dst[at];
+      r[u] = j0 + u < k ? row_of(d[u]) : m;
       wj[u] = w[at];
       acc[u] = 0.f;
     }
+    const int mine = j0 + (int)(threadIdx.x & (kJ - 1));
+    const int my_r = CODES && mine < k ? row_of(dst[p0 + mine]) : m;
     auto body = [&](auto whole, int piece) {
       constexpr bool kWhole = decltype(whole)::value;
       const int c = piece >> 4, c0 = piece_col<Row>(piece);
@@ -180,21 +188,20 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
       typename Row::Raw raw[kJ];
 #pragma unroll
       for (int u = 0; u < kJ; ++u)
-        if (j0 + u < k && row_ok(d[u], m))
-          raw[u] = load_piece<Row, kWhole, NTI>(yp + (int64_t)d[u] * ld_yp, c0, cols);
+        if (d[u] >= 0 && row_ok(r[u], m))
+          raw[u] = load_piece<Row, kWhole, NTI>(yp + (int64_t)r[u] * ld_yp, c0, cols);
       bool in[Row::kRuns];
 #pragma unroll
       for (int i = 0; i < Row::kRuns; ++i) in[i] = c0 + 64 * i < cols;
       float g[8];
       Row::unpack(graw, g);
+      uint32_t am[kJ];
 #pragma unroll
       for (int u = 0; u < kJ; ++u) {
-        if (j0 + u >= k) break;
-        const bool kept = d[u] >= 0;
-        const int r = kept ? d[u] : -1 - d[u];
-        if (!row_ok(r, m)) continue;
+        am[u] = 0;
+        if (!row_ok(r[u], m)) continue;
         float v[8];
-        if (kept) {
+        if (d[u] >= 0) {
           Row::unpack(raw[u], v);
 #pragma unroll
           for (int i = 0; i < Row::kRuns; ++i) {
@@ -203,24 +210,33 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
             for (int e = i * Row::kLen; e < (i + 1) * Row::kLen; ++e) part = __builtin_fmaf(g[e], v[e], part);
             acc[u] = in[i] ? part : acc[u];
           }
-        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = kept ? g[e] * wj[u] : 0.f;
-        const typename Row::Raw out = Row::pack(v);
-        if (ROWS) store_piece<Row, kWhole, NT>(rows + (int64_t)r * ld_r, c0, cols, out);
-        if (CODES) {
-          Row::unpack(out, v);  // the codes are those of the rounded row
-          uint32_t a = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) a = max(a, abs_bits(v[e]));
-          a = row16_max_u32(a);
-          float sc, inv;
-          group_scale(__uint_as_float(a), sc, inv);
-          store_codes<Row, kWhole, NT>(q + (int64_t)r * ld_q, c0, cols,
-                                       pack4_e4m3_grp(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
-                                       pack4_e4m3_grp(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
-          if ((piece & 15) == 0) s[(int64_t)r * ld_s + c] = sc;
+          for (int e = 0; e < 8; ++e) v[e] = g[e] * wj[u];
+          raw[u] = Row::pack(v);
+        } else {
+          raw[u] = typename Row::Raw{};
         }
+        if (ROWS) store_piece<Row, kWhole, NT>(rows + (int64_t)r[u] * ld_r, c0, cols, raw[u]);
+        if (CODES) am[u] = row16_max_u32(Row::max_bits(raw[u]));  // the codes are those of the rounded row
+      }
+      if (CODES) {
+        // lane u of the group forms the scale of row u
+        const int lig = piece & 15;
+        uint32_t a = am[0];
+#pragma unroll
+        for (int u = 1; u < kJ; ++u) a = (lig & 7) == u ? +am[u] : a;
+        float sc, inv;
+        group_scale(__uint_as_float(a), sc, inv);
+        if (lig < kJ && row_ok(my_r, m)) s[(int64_t)my_r * ld_s + c] = sc;
+        each_choice([&](auto u) {
+          if (!row_ok(r[u.value], m)) return;
+          const float iu = row_bcast<u.value>(inv);
+          float v[8];
+          Row::unpack(raw[u.value], v);
+          store_codes<Row, kWhole, NT>(q + (int64_t)r[u.value] * ld_q, c0, cols,
+                                       pack4_e4m3_grp(v[0] * iu, v[1] * iu, v[2] * iu, v[3] * iu),
+                                       pack4_e4m3_grp(v[4] * iu, v[5] * iu, v[6] * iu, v[7] * iu));
+        });
       }
     };
     for (int piece = piece0; (piece >> 4) * 128 < cols; piece += step) {

@@ -66,6 +66,15 @@ struct RowBF16 {
     for (int i = 0; i < 4; ++i) r.a[0][i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
     return r;
   }
+  // The largest magnitude as FP32 bits (a NaN is larger than all).
+  __device__ __forceinline__ static uint32_t max_bits(const Raw& r) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = __builtin_bit_cast(u16x2, r.a[0][0] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, r.a[0][i] & 0x7FFF7FFFu));
+    return (uint32_t)max(m[0], m[1]) << 16;
+  }
   __device__ __forceinline__ static float load1(const elem* p) { return bf16_to_f32(*p); }
   __device__ __forceinline__ static void store1(elem* p, float v) { *p = (elem)pack2_bf16(v, 0.f); }
 };
@@ -83,6 +92,12 @@ struct RowF32 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.a[i >> 2][i & 3] = __float_as_uint(v[i]);
     return r;
+  }
+  __device__ __forceinline__ static uint32_t max_bits(const Raw& r) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, r.a[i >> 2][i & 3] & 0x7FFFFFFFu);
+    return m;
   }
   __device__ __forceinline__ static float load1(const elem* p) { return *p; }
   __device__ __forceinline__ static void store1(elem* p, float v) { *p = v; }
