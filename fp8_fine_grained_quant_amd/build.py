@@ -108,7 +108,7 @@ def _build_calls(verbose):
     cmd += [os.path.join(CSRC, "calls.cpp"), "-o", tmp]
     for d in library_paths():
         cmd += ["-L" + d]
-    _run(cmd + ["-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"], verbose)
+    _run(cmd + ["-ltorch_python", "-ltorch_hip", "-ltorch", "-ltorch_cpu", "-lc10"], verbose)
     os.replace(tmp, CALLS)
 
 

@@ -11,7 +11,8 @@
 
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -135,9 +136,11 @@ T* data(const Tensor* t) { return t ? static_cast<T*>(t->data_ptr()) : nullptr; 
 template <class T>
 T* data(const Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 
-Tensor make(at::IntArrayRef sizes, ScalarType type, const Tensor& like) {
-  return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
+// What at::empty calls behind its dispatch, which is half of its 0.85 us.
+Tensor make(at::IntArrayRef sizes, ScalarType type, c10::Device device) {
+  return at::detail::empty_cuda(sizes, type, device, std::nullopt);
 }
+Tensor make(at::IntArrayRef sizes, ScalarType type, const Tensor& like) { return make(sizes, type, like.device()); }
 // `given`, or a new tensor that `own` keeps.
 const Tensor& given_or(const Tensor* given, Tensor& own, at::IntArrayRef sizes, ScalarType type, const Tensor& like) {
   if (given) return *given;
@@ -509,9 +512,8 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const double max_norm = real(a[2]);
   Tensor own_norm, own_ws;
   if (!norm) {
-    const at::TensorOptions options = at::TensorOptions().device(device);
-    own_norm = at::empty({}, options.dtype(at::kFloat));
-    own_ws = at::empty({lib.grad_clip_workspace(tensors)}, options.dtype(at::kByte));
+    own_norm = make({}, at::kFloat, device);
+    own_ws = make({lib.grad_clip_workspace(tensors)}, at::kByte, device);
     norm = &own_norm;
     ws = &own_ws;
   }
