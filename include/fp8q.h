@@ -518,8 +518,9 @@ fp8q_status fp8q_grouped_gemm_mx_dgrad(const uint8_t* dyq, const uint8_t* dys, c
  * the gradients of each step.  Limits: 1 <= k <= 32, k <= E <= 1024.
  * Logits, token rows and expert rows may start at any element and have any
  * row stride >= their length (no 16-byte rule here); ids, weights and maps
- * are contiguous [T, k].  Codes written with a row stride that is a multiple
- * of 16 bytes feed the grouped products and quantizers as they are.
+ * are contiguous [T, k].  Rows have at most 2^30 columns, and T * H / 8 stays
+ * below 2^31.  Codes written with a row stride that is a multiple of 16 bytes
+ * feed the grouped products and quantizers as they are.
  */
 typedef enum { FP8Q_SOFTMAX = 0, FP8Q_SIGMOID = 1 } fp8q_score;
 
@@ -537,7 +538,8 @@ typedef enum { FP8Q_SOFTMAX = 0, FP8Q_SIGMOID = 1 } fp8q_score;
  *   ids     : [T, k] int32, best first; -1 where a token has fewer than k
  *             experts that are not masked
  *   weights : [T, k] FP32: chosen score (renormalized) * scale, 0 beside id -1
- * A NaN logit is never chosen (softmax weights of its token are NaN).
+ * Logits are finite or -inf.  A NaN logit is never chosen; it makes the weights
+ * of its token's softmax NaN unless they are renormalized.
  */
 fp8q_status fp8q_moe_route(const void* logits, fp8q_dtype lt, int64_t T, int64_t E, int64_t ld, int k, int score,
                            const float* bias, int renormalize, float scale, int32_t* ids, float* weights,
@@ -622,6 +624,7 @@ fp8q_status fp8q_moe_combine_bwd(const void* dy, const void* yp, fp8q_dtype t, i
  * max_norm / norm (so a NaN norm gives NaN, an infinite one zeros and NaN).
  *   grads : HOST array (read during the call only) of n dense FP32 tensors of
  *           any length; out is of type ot, and may be g itself if ot is FP32
+ *           (then nothing is written where c = 1)
  *   max_norm : >= 0; +inf only measures and copies
  *   workspace : 8-byte aligned, fp8q_grad_clip_workspace(n) bytes
  *   norm  : one FP32, the norm before clipping
