@@ -765,7 +765,8 @@ fp8q_status fp8q_moe_combine_bwd(const void* dy, const void* yp, fp8q_dtype t, i
 
 int64_t fp8q_grad_clip_workspace(int64_t n) {
   if (n < 0 || n > kMaxDim) return -1;
-  return cdiv(n, fp8q::kMaxClipTensors) * fp8q::kClipBlocks * (int64_t)sizeof(double);
+  // per launch: partial sums, and the table the second pass reads
+  return cdiv(n, fp8q::kMaxClipTensors) * (fp8q::kClipBlocks * (int64_t)sizeof(double) + (int64_t)sizeof(fp8q::ClipBatch));
 }
 
 fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, double max_norm, void* workspace,
@@ -778,40 +779,49 @@ fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, dou
   int64_t chunks = 0;  // of all tensors: counted in 32 bits
   for (int64_t i = 0; i < n; ++i) {
     const fp8q_grad& g = grads[i];
-    if (g.len < 0 || (chunks += fp8q::clip_chunks(g.len)) > kMaxDim / 2) return FP8Q_ERR_SHAPE;
+    if (g.len < 0 || (chunks += cdiv(g.len, fp8q::kClipChunk)) > kMaxDim / 2) return FP8Q_ERR_SHAPE;
     if (g.len == 0) continue;
     if (!g.g || !g.out) return FP8Q_ERR_NULL;
     if (!aligned4(g.g) || !aligned_to(g.out, esize(ot))) return FP8Q_ERR_ALIGN;
   }
   // tables of up to kMaxClipTensors non-empty tensors, one launch each and pass
-  const bool bf16 = ot == FP8Q_BF16;
+  static_assert(sizeof(fp8q::ClipBatch) % 8 == 0, "tables follow each other");
   double* const part = static_cast<double*>(workspace);
-  int parts = 0;
+  fp8q::ClipBatch* const tables =
+      reinterpret_cast<fp8q::ClipBatch*>(part + cdiv(n, fp8q::kMaxClipTensors) * fp8q::kClipBlocks);
+  int parts = 0, batches = 0;
   fp8q::ClipBatch b;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t i = 0;
-    bool first = true;
-    do {
-      b.n = 0;
-      b.cum[0] = 0;
-      for (; i < n && b.n < fp8q::kMaxClipTensors; ++i) {
-        const int64_t c = fp8q::clip_chunks(grads[i].len);
-        if (c == 0) continue;
-        b.g[b.n] = grads[i].g; b.out[b.n] = grads[i].out; b.len[b.n] = grads[i].len;
-        b.cum[b.n + 1] = b.cum[b.n] + (int)c;
-        ++b.n;
-      }
-      hipError_t e = hipSuccess;
-      if (pass == 0) {
-        int blocks = 0;
-        if (b.n > 0) e = fp8q::launch_grad_sumsq(b, part + parts, &blocks, stream);
-        parts += blocks;
-      } else if (b.n > 0 || first) {
-        e = fp8q::launch_grad_scale(b, bf16, part, parts, max_norm, first ? norm : nullptr, stream);
-      }
-      if (e != hipSuccess) return FP8Q_ERR_LAUNCH;
-      first = false;
-    } while (i < n);
+  for (int64_t i = 0; i < n;) {
+    b.n = 0;
+    b.cum[0] = 0;
+    for (; i < n && b.n < fp8q::kMaxClipTensors; ++i) {
+      const int64_t len = grads[i].len, c = cdiv(len, fp8q::kClipChunk);
+      if (c == 0) continue;
+      b.g[b.n] = grads[i].g;
+      b.out[b.n] = grads[i].out;
+      b.last[b.n] = (uint16_t)(len - (c - 1) * fp8q::kClipChunk);
+      b.cum[b.n + 1] = b.cum[b.n] + (int)c;
+      ++b.n;
+    }
+    if (b.n == 0) break;
+    int blocks = 0;
+    if (fp8q::launch_grad_sumsq(b, tables + batches, part + parts, &blocks, stream) != hipSuccess)
+      return FP8Q_ERR_LAUNCH;
+    parts += blocks;
+    ++batches;
+  }
+  // the second pass of the batches before the last: counted again from the sizes
+  int64_t i = 0;
+  for (int k = 0; k < (batches > 0 ? batches : 1); ++k) {
+    int tensors = 0, chunk_count = 0;
+    for (; i < n && tensors < fp8q::kMaxClipTensors; ++i) {
+      const int c = (int)cdiv(grads[i].len, fp8q::kClipChunk);
+      tensors += c > 0;
+      chunk_count += c;
+    }
+    if (fp8q::launch_grad_scale(tables + k, chunk_count, ot == FP8Q_BF16, part, parts, max_norm,
+                                k == 0 ? norm : nullptr, stream) != hipSuccess)
+      return FP8Q_ERR_LAUNCH;
   }
   return FP8Q_OK;
 }

@@ -25,18 +25,29 @@ namespace fp8q {
 namespace {
 
 constexpr int kClipThreads = 256, kClipLoads = 8;
-constexpr int kClipStep = kClipThreads * 4;            // elements of one load of the whole block
-constexpr int kClipChunk = kClipStep * kClipLoads;     // elements of one tensor a block takes at a time
+constexpr int kClipStep = kClipThreads * 4;  // elements of one load of the whole block
+static_assert(kClipStep * kClipLoads == kClipChunk, "a chunk is one round of loads");
 
-// The tensor that chunk c belongs to: cum[i] is the first chunk of tensor i.
-__device__ __forceinline__ int clip_find(const ClipBatch& b, int c) {
-  int lo = 0, hi = b.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (c >= b.cum[mid]) lo = mid; else hi = mid;
+// Finds a chunk's tensor: a lane holds two of the tensors' first chunks, so
+// that the table is read once, not searched through its memory.
+template <int N>
+struct ClipFinder {
+  const ClipTable<N>& b;
+  int first0, first1;
+  __device__ __forceinline__ explicit ClipFinder(const ClipTable<N>& t) : b(t) {
+    constexpr int kNone = 0x7FFFFFFF;
+    const int lane = threadIdx.x & 63, n = t.n;
+    first0 = lane < n ? t.cum[lane < N ? lane : 0] : kNone;
+    first1 = N > 64 && lane + 64 < n ? t.cum[lane + 64 < N ? lane + 64 : 0] : kNone;
   }
-  return lo;
-}
+  // The tensor of chunk c, and where in it the chunk starts and how long it is.
+  __device__ __forceinline__ int operator()(int c, int64_t& lo, int& len) const {
+    const int i = __popcll(__ballot(first0 <= c)) + (N > 64 ? __popcll(__ballot(first1 <= c)) : 0) - 1;
+    lo = (int64_t)(c - b.cum[i]) * kClipChunk;
+    len = c + 1 < b.cum[i + 1] ? kClipChunk : (int)b.last[i];
+    return i;
+  }
+};
 
 __device__ __forceinline__ double block_sum(double v, double* red) {
 #pragma unroll
@@ -66,14 +77,31 @@ __device__ __forceinline__ void load_chunk(const float* g, int len, float (&v)[k
   }
 }
 
-__global__ __launch_bounds__(kClipThreads) void k_grad_sumsq(const ClipBatch b, double* __restrict__ part) {
+template <int N>
+__global__ __launch_bounds__(kClipThreads) void k_grad_sumsq(const ClipTable<N> b, ClipBatch* __restrict__ table,
+                                                             double* __restrict__ part) {
   __shared__ double red[4];
+  const ClipFinder<N> find(b);
+  if (blockIdx.x == gridDim.x - 1) {  // the second pass reads the table from memory
+    const int n = b.n;
+    for (int i = threadIdx.x; i <= n; i += kClipThreads) {
+      table->cum[i] = b.cum[i];
+      if (i < n) {
+        table->g[i] = b.g[i];
+        table->out[i] = b.out[i];
+        table->last[i] = b.last[i];
+      }
+    }
+    if (threadIdx.x == 0) table->n = (uint16_t)n;
+  }
   double s = 0;
-  for (int c = blockIdx.x; c < b.cum[b.n]; c += gridDim.x) {
-    const int i = clip_find(b, c);
-    const int64_t lo = (int64_t)(c - b.cum[i]) * kClipChunk;
+  const int chunks = b.cum[b.n];
+  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
+    int64_t lo;
+    int len;
+    const int i = find(c, lo, len);
     float v[kClipLoads][4];
-    load_chunk<0>(b.g[i] + lo, (int)min((int64_t)kClipChunk, b.len[i] - lo), v);
+    load_chunk<0>(b.g[i] + lo, len, v);
 #pragma unroll
     for (int l = 0; l < kClipLoads; ++l)
 #pragma unroll
@@ -102,22 +130,24 @@ __device__ __forceinline__ void store_clipped(void* out, int64_t at, const float
 }
 
 template <bool OUT_BF16>
-__global__ __launch_bounds__(kClipThreads) void k_grad_scale(const ClipBatch b, const double* __restrict__ part,
-                                                             int parts, double max_norm,
-                                                             float* __restrict__ norm_out) {
+__global__ __launch_bounds__(kClipThreads) void k_grad_scale(const ClipBatch* __restrict__ table, int chunks,
+                                                             const double* __restrict__ part, int parts,
+                                                             double max_norm, float* __restrict__ norm_out) {
   __shared__ double red[4];
+  const ClipBatch& b = *table;
   double s = 0;
   for (int i = threadIdx.x; i < parts; i += kClipThreads) s += part[i];
   const double norm = sqrt(block_sum(s, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   // a NaN norm fails the comparison and gives a NaN factor, an infinite one 0
   const float f = norm <= max_norm ? 1.f : (float)(max_norm / norm);
-  const int chunks = b.cum[b.n];
+  if (chunks == 0) return;  // no table
+  const ClipFinder<kMaxClipTensors> find(b);
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = clip_find(b, c);
+    int64_t lo;
+    int len;
+    const int i = find(c, lo, len);
     if (!OUT_BF16 && f == 1.f && b.out[i] == b.g[i]) continue;  // in place, and nothing to clip
-    const int64_t lo = (int64_t)(c - b.cum[i]) * kClipChunk;
-    const int len = (int)min((int64_t)kClipChunk, b.len[i] - lo);
     float v[kClipLoads][4];
     load_chunk<1>(b.g[i] + lo, len, v);
 #pragma unroll
@@ -132,27 +162,43 @@ __global__ __launch_bounds__(kClipThreads) void k_grad_scale(const ClipBatch b, 
 
 // Blocks of one launch: at most kClipBlocks, so that the partial sums every
 // scaling block adds up stay few.
-int clip_blocks(const ClipBatch& b) {
-  const int c = b.cum[b.n];
-  return c < 1 ? 1 : c < kClipBlocks ? c : kClipBlocks;
+int clip_blocks(int chunks) { return chunks < 1 ? 1 : chunks < kClipBlocks ? chunks : kClipBlocks; }
+
+template <int N>
+hipError_t sumsq(const ClipBatch& b, ClipBatch* table, double* part, int blocks, hipStream_t st) {
+  ClipTable<N> t;
+  t.n = b.n;
+  for (int i = 0; i < b.n; ++i) {
+    t.g[i] = b.g[i];
+    t.out[i] = b.out[i];
+    t.cum[i] = b.cum[i];
+    t.last[i] = b.last[i];
+  }
+  t.cum[b.n] = b.cum[b.n];
+  hipLaunchKernelGGL(k_grad_sumsq<N>, dim3(blocks), dim3(kClipThreads), 0, st, t, table, part);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t clip_chunks(int64_t len) { return (len + kClipChunk - 1) / kClipChunk; }
-
-hipError_t launch_grad_sumsq(const ClipBatch& b, double* part, int* blocks, hipStream_t st) {
-  *blocks = clip_blocks(b);
-  hipLaunchKernelGGL(k_grad_sumsq, dim3(*blocks), dim3(kClipThreads), 0, st, b, part);
-  return hipGetLastError();
+// The table's size is that of a few classes: a launch with 2.7 KB of arguments
+// takes 4.4 us on the host, one without 3.0.
+hipError_t launch_grad_sumsq(const ClipBatch& b, ClipBatch* table, double* part, int* blocks, hipStream_t st) {
+  *blocks = clip_blocks(b.cum[b.n]);
+  if (b.n <= 8) return sumsq<8>(b, table, part, *blocks, st);
+  if (b.n <= 32) return sumsq<32>(b, table, part, *blocks, st);
+  if (b.n <= 64) return sumsq<64>(b, table, part, *blocks, st);
+  return sumsq<kMaxClipTensors>(b, table, part, *blocks, st);
 }
 
-hipError_t launch_grad_scale(const ClipBatch& b, bool out_bf16, const double* part, int parts, double max_norm,
-                             float* norm, hipStream_t st) {
+hipError_t launch_grad_scale(const ClipBatch* table, int chunks, bool out_bf16, const double* part, int parts,
+                             double max_norm, float* norm, hipStream_t st) {
+  const dim3 grid(clip_blocks(chunks));
   if (out_bf16)
-    hipLaunchKernelGGL(k_grad_scale<true>, dim3(clip_blocks(b)), dim3(kClipThreads), 0, st, b, part, parts, max_norm, norm);
+    hipLaunchKernelGGL(k_grad_scale<true>, grid, dim3(kClipThreads), 0, st, table, chunks, part, parts, max_norm, norm);
   else
-    hipLaunchKernelGGL(k_grad_scale<false>, dim3(clip_blocks(b)), dim3(kClipThreads), 0, st, b, part, parts, max_norm, norm);
+    hipLaunchKernelGGL(k_grad_scale<false>, grid, dim3(kClipThreads), 0, st, table, chunks, part, parts, max_norm,
+                       norm);
   return hipGetLastError();
 }
 

@@ -169,16 +169,21 @@ hipError_t launch_moe_combine_bwd(const MoeRows& a, const void* dy, int64_t ld_d
 // ------------------------------------------------------- gradient clipping
 constexpr int kMaxClipTensors = 96;  // per launch: the table travels in the kernel's arguments
 constexpr int kClipBlocks = 2048;    // most blocks, and partial sums, per launch
-struct ClipBatch {
-  int n;
-  int cum[kMaxClipTensors + 1];  // first chunk of each tensor, then their number
-  const float* g[kMaxClipTensors];
-  void* out[kMaxClipTensors];
-  int64_t len[kMaxClipTensors];
+constexpr int kClipChunk = 8192;     // elements of one tensor a block takes at a time
+// Up to N tensors, none of them empty.
+template <int N>
+struct ClipTable {
+  const float* g[N];
+  void* out[N];
+  int cum[N + 1];    // first chunk of each tensor, then their number
+  uint16_t last[N];  // elements of a tensor's last chunk
+  uint16_t n;
 };
-int64_t clip_chunks(int64_t len);  // chunks a tensor is cut into
-hipError_t launch_grad_sumsq(const ClipBatch& b, double* part, int* blocks, hipStream_t st);
-hipError_t launch_grad_scale(const ClipBatch& b, bool out_bf16, const double* part, int parts, double max_norm,
-                             float* norm, hipStream_t st);
+typedef ClipTable<kMaxClipTensors> ClipBatch;
+// The sums of squares of the batch's chunks, *blocks of them; leaves the table
+// in `table` (device memory) for the second pass.
+hipError_t launch_grad_sumsq(const ClipBatch& b, ClipBatch* table, double* part, int* blocks, hipStream_t st);
+hipError_t launch_grad_scale(const ClipBatch* table, int chunks, bool out_bf16, const double* part, int parts,
+                             double max_norm, float* norm, hipStream_t st);
 
 }  // namespace fp8q
