@@ -40,7 +40,6 @@ moe_dispatch, moe_dispatch_quant, moe_dispatch_bwd, moe_combine,
 moe_combine_bwd, moe_combine_bwd_quant, grad_clip.
 """
 
-import contextlib
 import ctypes
 import os
 
@@ -788,24 +787,15 @@ def _bind(lib):
     from . import _calls
     names = [n for n in EXPORTS if n.startswith(("fp8q_moe_", "fp8q_grad_"))]
     _calls.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _current_device,
-                _current_stream, _check)
+                _current_stream, _check, _score, _on_stream)
     return _calls
 
 
-def _handle(stream):
-    return None if stream is None else _stream(stream)
-
-
-def _on(stream, call, *args):
-    """call(*args, stream's handle), which allocates on the stream it runs on,
-    so that the caching allocator hands memory freed at the call's end only to
-    later work of that stream."""
-    if stream is None:
-        return call(*args, None)
-    handle = _stream(stream)
-    side = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle)
+def _on_stream(name, args, stream):
+    """The native call `name` with `stream` as torch's current stream."""
+    side = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(side):
-        return call(*args, handle)
+        return getattr(_bound, name)(*args, None)
 
 
 def _required(**outputs):
@@ -818,13 +808,13 @@ def fp8q_moe_route(logits, ids, weights, score="softmax", bias=None, renormalize
     """The k = ids.shape[1] best experts of every token: ids [T, k] int32,
     weights [T, k] FP32 from logits [T, E] (BF16 or FP32)."""
     _required(ids=ids, weights=weights)
-    _native().moe_route(logits, 0, _score(score), bias, bool(renormalize), scale, ids, weights, _handle(stream))
+    _native().moe_route(logits, 0, score, bias, renormalize, scale, ids, weights, stream)
 
 
 def fp8q_moe_route_bwd(dweights, logits, ids, dlogits, score="softmax", renormalize=True, scale=1.0, stream=None):
     """Gradient of the weights to the logits, dlogits [T, E] of the logits' type."""
     _required(dlogits=dlogits)
-    _native().moe_route_bwd(dweights, logits, ids, _score(score), bool(renormalize), scale, dlogits, _handle(stream))
+    _native().moe_route_bwd(dweights, logits, ids, score, renormalize, scale, dlogits, stream)
 
 
 def moe_sort_workspace(pairs, experts):
@@ -840,32 +830,32 @@ def fp8q_moe_sort(ids, experts, offsets, dst, src=None, workspace=None, cover=Fa
     pair, or -1 - row for a dropped one), src [T*k] the pair of each row.
     workspace: moe_sort_workspace(T*k, experts) bytes (uint8), None if 0."""
     _required(offsets=offsets, dst=dst)
-    _native().moe_sort(ids, experts, bool(cover), offsets, dst, src, workspace, _handle(stream))
+    _native().moe_sort(ids, experts, cover, offsets, dst, src, workspace, stream)
 
 
 def fp8q_moe_dispatch(x, dst, rows=None, q=None, scale=None, stream=None):
     """Token rows x [T, H] into expert order: rows [T*k, H] and/or their 1x128
     codes and scales; zeros for dropped pairs."""
-    _native().moe_dispatch(x, dst, rows, q, scale, 0, _handle(stream))
+    _native().moe_dispatch(x, dst, rows, q, scale, None, stream)
 
 
 def fp8q_moe_dispatch_bwd(drows, dst, dx, stream=None):
     """dx [T, H] = sum of each token's kept rows of drows [T*k, H]."""
     _required(dx=dx)
-    _native().moe_dispatch_bwd(drows, dst, dx, _handle(stream))
+    _native().moe_dispatch_bwd(drows, dst, dx, stream)
 
 
 def fp8q_moe_combine(yp, dst, weights, y, stream=None):
     """y [T, H] = weighted sum of each token's kept rows of yp [T*k, H]."""
     _required(y=y)
-    _native().moe_combine(yp, dst, weights, y, _handle(stream))
+    _native().moe_combine(yp, dst, weights, y, stream)
 
 
 def fp8q_moe_combine_bwd(dy, yp, dst, weights, dweights, rows=None, q=None, scale=None, stream=None):
     """Gradients of the combination: rows [T*k, H] (to yp) and/or their codes
     and scales, dweights [T, k]."""
     _required(dweights=dweights)
-    _native().moe_combine_bwd(dy, yp, dst, weights, dweights, rows, q, scale, 0, _handle(stream))
+    _native().moe_combine_bwd(dy, yp, dst, weights, dweights, rows, q, scale, 0, stream)
 
 
 def grad_clip_workspace(n):
@@ -878,25 +868,25 @@ def fp8q_grad_clip(grads, out, max_norm, norm, workspace, stream=None):
     clipping), out[i] = grads[i] * min(1, max_norm / norm), all FP32 or all
     BF16, grads[i] itself for clipping in place.
     workspace: grad_clip_workspace(len(grads)) bytes (uint8)."""
-    _required(norm=norm, workspace=workspace)
-    _native().grad_clip(grads, out, max_norm, norm, workspace, _handle(stream))
+    _required(out=out, norm=norm, workspace=workspace)
+    _native().grad_clip(grads, out, max_norm, norm, workspace, stream)
 
 
 def moe_route(logits, k, score="softmax", bias=None, renormalize=True, scale=1.0, stream=None):
     """The k best experts of every token and their weights: (ids, weights)."""
-    return _on(stream, _native().moe_route, logits, k, _score(score), bias, bool(renormalize), scale, None, None)
+    return _native().moe_route(logits, k, score, bias, renormalize, scale, None, None, stream)
 
 
 def moe_route_bwd(dweights, logits, ids, score="softmax", renormalize=True, scale=1.0, stream=None):
     """Gradient of moe_route's weights to the logits, for the ids it chose."""
-    return _on(stream, _native().moe_route_bwd, dweights, logits, ids, _score(score), bool(renormalize), scale, None)
+    return _native().moe_route_bwd(dweights, logits, ids, score, renormalize, scale, None, stream)
 
 
 def moe_sort(ids, experts, cover=False, stream=None):
     """The pairs of ids [T, k] in expert order: (offsets, dst, src).  cover:
     dropped pairs' rows (zeros) count as the last expert's, as the grouped
     products' offsets need it where pairs are dropped."""
-    return _on(stream, _native().moe_sort, ids, experts, bool(cover), None, None, None, None)
+    return _native().moe_sort(ids, experts, cover, None, None, None, None, stream)
 
 
 _ROWS, _CODES = 1, 2
@@ -904,28 +894,28 @@ _ROWS, _CODES = 1, 2
 
 def moe_dispatch(x, dst, stream=None):
     """Token rows into expert order (zeros for dropped pairs)."""
-    return _on(stream, _native().moe_dispatch, x, dst, None, None, None, _ROWS)[0]
+    return _native().moe_dispatch(x, dst, None, None, None, _ROWS, stream)[0]
 
 
 def moe_dispatch_quant(x, dst, with_output=True, stream=None):
     """Dispatch with the 1x128 quantization of the rows: (rows or None, q, scale)."""
     want = _ROWS | _CODES if with_output else _CODES
-    return _on(stream, _native().moe_dispatch, x, dst, None, None, None, want)
+    return _native().moe_dispatch(x, dst, None, None, None, want, stream)
 
 
 def moe_dispatch_bwd(drows, dst, stream=None):
     """Gradient of moe_dispatch: the sum of each token's kept rows."""
-    return _on(stream, _native().moe_dispatch_bwd, drows, dst, None)
+    return _native().moe_dispatch_bwd(drows, dst, None, stream)
 
 
 def moe_combine(yp, dst, weights, stream=None):
     """Expert rows back into token order with the weights applied."""
-    return _on(stream, _native().moe_combine, yp, dst, weights, None)
+    return _native().moe_combine(yp, dst, weights, None, stream)
 
 
 def moe_combine_bwd(dy, yp, dst, weights, stream=None):
     """Gradients of moe_combine: (rows, dweights)."""
-    out = _on(stream, _native().moe_combine_bwd, dy, yp, dst, weights, None, None, None, None, _ROWS)
+    out = _native().moe_combine_bwd(dy, yp, dst, weights, None, None, None, None, _ROWS, stream)
     return out[0], out[3]
 
 
@@ -933,7 +923,7 @@ def moe_combine_bwd_quant(dy, yp, dst, weights, with_output=True, stream=None):
     """Gradients of moe_combine, those to the expert rows also (or only) as
     1x128 codes: (rows or None, q, scale, dweights)."""
     want = _ROWS | _CODES if with_output else _CODES
-    return _on(stream, _native().moe_combine_bwd, dy, yp, dst, weights, None, None, None, None, want)
+    return _native().moe_combine_bwd(dy, yp, dst, weights, None, None, None, None, want, stream)
 
 
 # ----------------------------------------------------------- gradient clipping
@@ -941,4 +931,4 @@ def grad_clip(grads, max_norm, out=None, stream=None):
     """Clips the FP32 gradients by their global norm into `out` (FP32 or BF16
     tensors of their shapes; None: in place).  Returns the norm before
     clipping, a 0-dim tensor on the GPU."""
-    return _on(stream, _native().grad_clip, grads, grads if out is None else out, max_norm, None, None)
+    return _native().grad_clip(grads, out, max_norm, None, None, stream)

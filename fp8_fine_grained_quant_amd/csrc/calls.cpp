@@ -6,8 +6,10 @@
 // whose kernels are shorter than that.
 //
 // Each function takes its arguments by position.  Outputs given as None are
-// allocated (on torch's current stream: the caller sets it where the call is
-// to run on another); a stream given as None is torch's current one.
+// allocated; a stream given as None is torch's current one.  A call that
+// allocates and is to run on another stream is made once more with that one as
+// torch's current stream, so that the caching allocator hands memory freed at
+// the call's end only to later work of that stream.
 
 #include <Python.h>
 
@@ -44,7 +46,7 @@ struct Library {
   decltype(&fp8q_grad_clip) grad_clip;
   decltype(&fp8q_grad_clip_workspace) grad_clip_workspace;
 } lib;
-PyObject *current_device, *current_stream, *raise_status;  // Python callables
+PyObject *current_device, *current_stream, *raise_status, *score_code, *on_stream;  // Python callables
 
 // ------------------------------------------------------------------ arguments
 [[noreturn]] void refuse(PyObject* type, const std::string& text) {
@@ -78,6 +80,20 @@ int64_t integer(PyObject* o) {
 int small(PyObject* o) {  // out of range stays out of range
   const int64_t v = integer(o);
   return v < 0 ? -1 : v > std::numeric_limits<int>::max() ? std::numeric_limits<int>::max() : (int)v;
+}
+int truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v;
+}
+int score_of(PyObject* o) {
+  if (PyUnicode_Check(o)) {
+    if (PyUnicode_CompareWithASCIIString(o, "softmax") == 0) return FP8Q_SOFTMAX;
+    if (PyUnicode_CompareWithASCIIString(o, "sigmoid") == 0) return FP8Q_SIGMOID;
+  }
+  THPObjectPtr r(PyObject_CallFunctionObjArgs(score_code, o, nullptr));  // refuses
+  if (!r) throw python_error();
+  return small(r.get());
 }
 double real(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
@@ -149,19 +165,38 @@ const Tensor& given_or(const Tensor* given, Tensor& own, at::IntArrayRef sizes, 
 }
 
 // ---------------------------------------------------------------------- calls
+hipStream_t handle_of(PyObject* o) {
+  void* p = PyLong_AsVoidPtr(o);
+  if (!p && PyErr_Occurred()) throw python_error();
+  return static_cast<hipStream_t>(p);
+}
+// None, a torch stream or a pointer as a number.
 hipStream_t stream_of(PyObject* o) {
   if (o != Py_None) {
-    void* p = PyLong_AsVoidPtr(o);
-    if (!p && PyErr_Occurred()) throw python_error();
-    return static_cast<hipStream_t>(p);
+    if (PyLong_Check(o)) return handle_of(o);
+    THPObjectPtr handle(PyObject_GetAttrString(o, "cuda_stream"));
+    if (!handle) throw python_error();
+    return handle_of(handle.get());
   }
   THPObjectPtr device(PyObject_CallNoArgs(current_device));
   if (!device) throw python_error();
   THPObjectPtr handle(PyObject_CallFunctionObjArgs(current_stream, device.get(), nullptr));
   if (!handle) throw python_error();
-  void* p = PyLong_AsVoidPtr(handle.get());
-  if (!p && PyErr_Occurred()) throw python_error();
-  return static_cast<hipStream_t>(p);
+  return handle_of(handle.get());
+}
+
+// The call of `name` with these arguments but the last, the stream, which is
+// torch's current one meanwhile.
+PyObject* again_on(const char* name, PyObject* const* a, Py_ssize_t n) {
+  THPObjectPtr args(PyTuple_New(n - 1));
+  if (!args) throw python_error();
+  for (Py_ssize_t i = 0; i + 1 < n; ++i) {
+    Py_INCREF(a[i]);
+    PyTuple_SET_ITEM(args.get(), i, a[i]);
+  }
+  PyObject* r = PyObject_CallFunction(on_stream, "sOO", name, args.get(), a[n - 1]);
+  if (!r) throw python_error();
+  return r;
 }
 
 void check(fp8q_status status, const char* name) {
@@ -207,6 +242,9 @@ PyObject* none() {
 PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 9);
+  if (a[6] == Py_None && a[n - 1] != Py_None) return again_on("moe_route", a, n);
+  const int score = score_of(a[2]), renorm = truth(a[4]);
+  const float scale = (float)real(a[5]);
   const Tensor &logits = tensor(a[0], "logits");
   const Tensor *bias = optional(a[3], "bias"), *ids = optional(a[6], "ids"), *weights = optional(a[7], "weights");
   matrix(logits, "logits");
@@ -226,8 +264,6 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor own_ids, own_weights;
   const Tensor& i = given_or(ids, own_ids, {tokens, k}, at::kInt, logits);
   const Tensor& w = given_or(weights, own_weights, {tokens, k}, at::kFloat, logits);
-  const int score = small(a[2]), renorm = small(a[4]);
-  const float scale = (float)real(a[5]);
   const hipStream_t st = stream_of(a[8]);
   check(unlocked([&] {
           return lib.moe_route(data<void>(logits), type, tokens, experts, ld, k, score, data<float>(bias), renorm,
@@ -243,6 +279,9 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* moe_route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 8);
+  if (a[6] == Py_None && a[n - 1] != Py_None) return again_on("moe_route_bwd", a, n);
+  const int score = score_of(a[3]), renorm = truth(a[4]);
+  const float scale = (float)real(a[5]);
   const Tensor &dweights = tensor(a[0], "dweights"), &logits = tensor(a[1], "logits"), &ids = tensor(a[2], "ids");
   const Tensor* dlogits = optional(a[6], "dlogits");
   matrix(logits, "logits");
@@ -257,8 +296,6 @@ PyObject* moe_route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor own;
   const Tensor& d = given_or(dlogits, own, {tokens, experts}, logits.scalar_type(), logits);
   const int64_t ld = stride(logits), ld_d = stride(d);
-  const int score = small(a[3]), renorm = small(a[4]);
-  const float scale = (float)real(a[5]);
   const hipStream_t st = stream_of(a[7]);
   check(unlocked([&] {
           return lib.moe_route_bwd(data<float>(dweights), data<void>(logits), type, tokens, experts, ld,
@@ -274,6 +311,7 @@ PyObject* moe_route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 8);
+  if (a[3] == Py_None && a[n - 1] != Py_None) return again_on("moe_sort", a, n);
   const Tensor& ids = tensor(a[0], "ids");
   const Tensor *offsets = optional(a[3], "offsets"), *dst = optional(a[4], "dst"), *src = optional(a[5], "src"),
                *ws = optional(a[6], "workspace");
@@ -287,7 +325,7 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   on_gpu({&ids, offsets, dst, src, ws});
   dense({&ids, offsets, dst, src, ws});
-  const int cover = small(a[2]);
+  const int cover = truth(a[2]);
   Tensor own_offsets, own_dst, own_src, own_ws;
   if (!offsets) {
     const int64_t need = lib.moe_sort_workspace(pairs, experts);
@@ -315,12 +353,9 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
 struct RowOutputs {
   const Tensor *rows, *q, *scale;
   Tensor own_rows, own_q, own_scale;
-  bool given;
 
   RowOutputs(PyObject* r, PyObject* c, PyObject* s)
-      : rows(optional(r, "rows")), q(optional(c, "q")), scale(optional(s, "scale")) {
-    given = rows || q || scale;
-  }
+      : rows(optional(r, "rows")), q(optional(c, "q")), scale(optional(s, "scale")) {}
   void expect_all(int64_t m, int64_t cols, ScalarType type) {
     if (rows) expect(rows, {m, cols}, type, "rows");
     if (q || scale) {
@@ -331,7 +366,6 @@ struct RowOutputs {
   // Codes in rows that are a multiple of 16 bytes apart, as the grouped
   // products take them.
   void allocate(int want, int64_t m, int64_t cols, const Tensor& like) {
-    if (given) return;
     if (want & 1) rows = &given_or(nullptr, own_rows, {m, cols}, like.scalar_type(), like);
     if (want & 2) {
       own_q = make({m, (cols + 15) / 16 * 16}, at::kByte, like);
@@ -346,10 +380,11 @@ struct RowOutputs {
 };
 PyObject* wrap_or_none(const Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : none(); }
 
-// x, dst, rows, q, scale, want, stream
+// x, dst, rows, q, scale, want, stream; with want None the outputs are given
 PyObject* moe_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 7);
+  if (a[5] != Py_None && a[n - 1] != Py_None) return again_on("moe_dispatch", a, n);
   const Tensor &x = tensor(a[0], "x"), &dst = tensor(a[1], "dst");
   RowOutputs out(a[2], a[3], a[4]);
   matrix(x, "x");
@@ -360,7 +395,7 @@ PyObject* moe_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   on_gpu({&x, &dst, out.rows, out.q, out.scale});
   dense({&dst});
   const fp8q_dtype type = type_of(x);
-  out.allocate(small(a[5]), m, cols, x);
+  if (a[5] != Py_None) out.allocate(small(a[5]), m, cols, x);
   const int64_t ld = stride(x), ld_r = out.ld_rows(), ld_q = out.ld_q(), ld_s = out.ld_scale();
   const hipStream_t st = stream_of(a[6]);
   check(unlocked([&] {
@@ -369,7 +404,7 @@ PyObject* moe_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                   ld_s, st);
         }),
         "fp8q_moe_dispatch");
-  if (out.given) return none();
+  if (a[5] == Py_None) return none();
   return pack({wrap_or_none(out.own_rows), wrap_or_none(out.own_q), wrap_or_none(out.own_scale)});
   END_HANDLE_TH_ERRORS
 }
@@ -378,6 +413,7 @@ PyObject* moe_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* moe_dispatch_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 4);
+  if (a[2] == Py_None && a[n - 1] != Py_None) return again_on("moe_dispatch_bwd", a, n);
   const Tensor &drows = tensor(a[0], "drows"), &dst = tensor(a[1], "dst");
   const Tensor* dx = optional(a[2], "dx");
   matrix(drows, "drows");
@@ -405,6 +441,7 @@ PyObject* moe_dispatch_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 5);
+  if (a[3] == Py_None && a[n - 1] != Py_None) return again_on("moe_combine", a, n);
   const Tensor &yp = tensor(a[0], "yp"), &dst = tensor(a[1], "dst"), &weights = tensor(a[2], "weights");
   const Tensor* out = optional(a[3], "y");
   matrix(yp, "yp");
@@ -434,6 +471,7 @@ PyObject* moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* moe_combine_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 10);
+  if (a[4] == Py_None && a[n - 1] != Py_None) return again_on("moe_combine_bwd", a, n);
   const Tensor &dy = tensor(a[0], "dy"), &yp = tensor(a[1], "yp"), &dst = tensor(a[2], "dst"),
                &weights = tensor(a[3], "weights");
   const Tensor* dweights = optional(a[4], "dweights");
@@ -466,14 +504,15 @@ PyObject* moe_combine_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// grads, out, max_norm, norm, workspace, stream (grads, out: sequences); with
-// norm None it and the workspace are allocated
+// grads, out, max_norm, norm, workspace, stream (grads, out: sequences; out
+// None: in place); with norm None it and the workspace are allocated
 PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 6);
+  if (a[3] == Py_None && a[n - 1] != Py_None) return again_on("grad_clip", a, n);
   THPObjectPtr grads(PySequence_Fast(a[0], "grads: expected a sequence of tensors"));
   if (!grads) throw python_error();
-  THPObjectPtr outs(PySequence_Fast(a[1], "out: expected a sequence of tensors"));
+  THPObjectPtr outs(PySequence_Fast(a[1] == Py_None ? grads.get() : a[1], "out: expected a sequence of tensors"));
   if (!outs) throw python_error();
   const Py_ssize_t tensors = PySequence_Fast_GET_SIZE(grads.get());
   if (PySequence_Fast_GET_SIZE(outs.get()) != tensors)
@@ -527,10 +566,10 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// {name: address}, current_device, current_stream, raise_status
+// {name: address}, current_device, current_stream, raise_status, score_code, on_stream
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  count(n, 4);
+  count(n, 6);
   auto find = [&](auto& f, const char* name) {
     PyObject* o = PyDict_GetItemString(a[0], name);
     void* p = o ? PyLong_AsVoidPtr(o) : nullptr;
@@ -547,8 +586,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   find(lib.moe_combine_bwd, "fp8q_moe_combine_bwd");
   find(lib.grad_clip, "fp8q_grad_clip");
   find(lib.grad_clip_workspace, "fp8q_grad_clip_workspace");
-  PyObject** const slots[] = {&current_device, &current_stream, &raise_status};
-  for (int i = 0; i < 3; ++i) {
+  PyObject** const slots[] = {&current_device, &current_stream, &raise_status, &score_code, &on_stream};
+  for (int i = 0; i < 5; ++i) {
     Py_INCREF(a[1 + i]);
     Py_XDECREF(*slots[i]);
     *slots[i] = a[1 + i];
