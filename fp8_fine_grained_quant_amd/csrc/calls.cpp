@@ -205,14 +205,16 @@ void check(fp8q_status status, const char* name) {
   throw python_error();
 }
 
-// The library's call without the interpreter's lock, as a foreign call has it.
+// The library's call without the interpreter's lock, as a foreign call has it;
+// the lock comes back also where a tensor has no memory to point to and throws.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 template <class F>
 fp8q_status unlocked(F f) {
-  fp8q_status s;
-  Py_BEGIN_ALLOW_THREADS
-  s = f();
-  Py_END_ALLOW_THREADS
-  return s;
+  Unlocked guard;
+  return f();
 }
 
 void count(Py_ssize_t n, Py_ssize_t want) {

@@ -66,6 +66,22 @@ def test_shapes_and_types():
     refused(TypeError, "yp: dtype torch.bfloat16", lambda: fq.moe_combine_bwd(z(6, 8), z(24, 8, dt=bf16), IDS, W))
 
 
+def test_tensors_without_memory():
+    """A tensor that only has a shape is refused by an exception, with the
+    interpreter's lock held again."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode(allow_non_fake_inputs=True):
+        x, ids, w = torch.empty(6, 32, device="cuda"), torch.empty(6, 4, dtype=i32, device="cuda"), \
+            torch.empty(6, 4, device="cuda")
+    for fn in (lambda: fq.fp8q_moe_route(x, ids, w), lambda: fq.fp8q_moe_route_bwd(w, x, ids, x),
+               lambda: fq.fp8q_moe_sort(ids, 4, torch.empty_like(ids).view(-1)[:5], ids),
+               lambda: fq.moe_combine(torch.empty_like(x), ids, w)):
+        with pytest.raises((RuntimeError, ValueError, TypeError)):
+            fn()
+    meta = torch.empty(6, 32, device="meta")
+    refused(ValueError, "GPU tensors only", lambda: fq.moe_route(meta, 2))
+
+
 @pytest.mark.gpu
 def test_refusals_on_the_gpu():
     d = lambda t: t.cuda()
