@@ -60,7 +60,7 @@ __device__ __forceinline__ int piece_col(int piece) { return (piece >> 4) * 128 
 // Dispatch: 16 lanes own one 128-column group of one token, so the group's
 // max-abs is one DPP row reduction (as k_quant_act) and a token is read and
 // quantized once however many rows it goes to.
-template <class Row, bool ROWS, bool CODES, bool WIDE, int NT>
+template <class Row, bool ROWS, bool CODES, bool WIDE, int PAST>
 __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_dispatch(
     const typename Row::elem* __restrict__ x, int64_t ld_x, const int* __restrict__ dst, int tokens, int k, int m,
     typename Row::elem* __restrict__ rows, int64_t ld_r, uint8_t* __restrict__ q, int64_t ld_q,
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_dispatch(
   const int* d = dst + (int64_t)t * k;
   auto body = [&](auto whole) {
     constexpr bool kWhole = decltype(whole)::value;
-    const typename Row::Raw raw = load_piece<Row, kWhole, 0>(x + (int64_t)t * ld_x, c0, cols);
+    const typename Row::Raw raw = load_piece<Row, kWhole, !WIDE, 0>(x + (int64_t)t * ld_x, c0, cols);
     uint32_t w0 = 0, w1 = 0;
     float sc = 0.f;
     if (CODES) {
@@ -97,10 +97,10 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_dispatch(
         if (ROWS) {
           typename Row::Raw z{};
           if (kept) z = raw;
-          store_piece<Row, kWhole, NT>(rows + (int64_t)r * ld_r, c0, cols, z);
+          store_piece<Row, kWhole, PAST & 1>(rows + (int64_t)r * ld_r, c0, cols, z);
         }
         if (CODES) {
-          store_codes<Row, kWhole, NT>(q + (int64_t)r * ld_q, c0, cols, kept ? w0 : 0u, kept ? w1 : 0u);
+          store_codes<Row, kWhole, PAST / 2>(q + (int64_t)r * ld_q, c0, cols, kept ? w0 : 0u, kept ? w1 : 0u);
           if ((piece & 15) == 0) s[(int64_t)r * ld_s + c] = kept ? sc : kAmaxFloor / kFp8Max;
         }
       }
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_gather(
       }
 #pragma unroll
       for (int u = 0; u < kJ; ++u)
-        if (row_ok(r[u], m)) raw[u] = load_piece<Row, kWhole, NT>(rows + (int64_t)r[u] * ld_r, c0, cols);
+        if (row_ok(r[u], m)) raw[u] = load_piece<Row, kWhole, !WIDE, NT>(rows + (int64_t)r[u] * ld_r, c0, cols);
 #pragma unroll
       for (int u = 0; u < kJ; ++u)
         if (row_ok(r[u], m)) {
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_gather(
 // ---------------------------------------------------------------------------
 // Combine backward: a token's products with its rows are summed inside one
 // block (WIDE) or one 16-lane group, without atomics: the order is fixed.
-template <class Row, bool ROWS, bool CODES, bool WIDE, int NT, int NTI>
+template <class Row, bool ROWS, bool CODES, bool WIDE, int PAST, int NTI>
 __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
     const typename Row::elem* __restrict__ dy, int64_t ld_dy, const typename Row::elem* __restrict__ yp,
     int64_t ld_yp, const int* __restrict__ dst, const float* __restrict__ w, int tokens, int k, int m,
@@ -184,15 +184,15 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
     auto body = [&](auto whole, int piece) {
       constexpr bool kWhole = decltype(whole)::value;
       const int c = piece >> 4, c0 = piece_col<Row>(piece);
-      const typename Row::Raw graw = load_piece<Row, kWhole, NTI>(dy + (int64_t)t * ld_dy, c0, cols);
+      const typename Row::Raw graw = load_piece<Row, kWhole, !WIDE, NTI>(dy + (int64_t)t * ld_dy, c0, cols);
       typename Row::Raw raw[kJ];
 #pragma unroll
       for (int u = 0; u < kJ; ++u)
         if (d[u] >= 0 && row_ok(r[u], m))
-          raw[u] = load_piece<Row, kWhole, NTI>(yp + (int64_t)r[u] * ld_yp, c0, cols);
+          raw[u] = load_piece<Row, kWhole, !WIDE, NTI>(yp + (int64_t)r[u] * ld_yp, c0, cols);
       bool in[Row::kRuns];
 #pragma unroll
-      for (int i = 0; i < Row::kRuns; ++i) in[i] = c0 + 64 * i < cols;
+      for (int i = 0; i < Row::kRuns; ++i) in[i] = !kWhole || c0 + 64 * i < cols;
       float g[8];
       Row::unpack(graw, g);
       uint32_t am[kJ];
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
         } else {
           raw[u] = typename Row::Raw{};
         }
-        if (ROWS) store_piece<Row, kWhole, NT>(rows + (int64_t)r[u] * ld_r, c0, cols, raw[u]);
+        if (ROWS) store_piece<Row, kWhole, PAST & 1>(rows + (int64_t)r[u] * ld_r, c0, cols, raw[u]);
         if (CODES) am[u] = row16_max_u32(Row::max_bits(raw[u]));  // the codes are those of the rounded row
       }
       if (CODES) {
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
           const float iu = row_bcast<u.value>(inv);
           float v[8];
           Row::unpack(raw[u.value], v);
-          store_codes<Row, kWhole, NT>(q + (int64_t)r[u.value] * ld_q, c0, cols,
+          store_codes<Row, kWhole, PAST / 2>(q + (int64_t)r[u.value] * ld_q, c0, cols,
                                        pack4_e4m3_grp(v[0] * iu, v[1] * iu, v[2] * iu, v[3] * iu),
                                        pack4_e4m3_grp(v[4] * iu, v[5] * iu, v[6] * iu, v[7] * iu));
         });
@@ -289,16 +289,17 @@ Shape shape_of(int64_t cols) {
   return h;
 }
 
-// Output runs that are aligned to their own size, in rows a multiple of that
-// apart, make whole segments, which are stored past the caches: the combine
-// gradient of 32768 rows of 7168 takes 246 us so and 271 us through them, the
-// dispatch to 16384 rows 69 and 81.  Cut segments lose by it (rows of 2047
-// BF16 columns: 21 us through the caches, 30 past them).
-bool aligned_out(const MoeRows& a) {
-  auto on = [](const void* p, int64_t row_bytes, int to) {
-    return !p || (reinterpret_cast<uintptr_t>(p) % to == 0 && row_bytes % to == 0);
+// Which outputs are stored past the caches (1: rows, 2: codes): those whose
+// rows start and end on whole 64-byte segments.  The combine gradient of 32768
+// rows of 7168 takes 246 us so and 271 us through the caches, the dispatch to
+// 16384 rows 69 and 81.  Cut segments lose by it: codes of 864 columns 35 us so
+// and 31 through the caches, of 832 columns 24 and 30; rows of 2047 BF16
+// columns 30 and 21.
+int past_caches(const MoeRows& a) {
+  auto whole = [](const void* p, int64_t row_bytes) {
+    return p && reinterpret_cast<uintptr_t>(p) % 64 == 0 && row_bytes % 64 == 0;
   };
-  return on(a.rows, a.ld_rows * (a.bf16 ? 2 : 4), 16) && on(a.q, a.ld_q, a.bf16 ? 8 : 4);
+  return (whole(a.rows, a.ld_rows * (a.bf16 ? 2 : 4)) ? 1 : 0) | (whole(a.q, a.ld_q) ? 2 : 0);
 }
 
 template <class F>
@@ -309,12 +310,22 @@ template <class F>
 void with_row(bool bf16, F f) {
   if (bf16) f(RowBF16{}); else f(RowF32{});
 }
-// The outputs asked for: rows, codes or both.
+// The outputs asked for (rows, codes or both) and which of them past the
+// caches; codes alone of both are stored through them with the rows.
 template <class F>
 void with_outputs(const MoeRows& a, F f) {
-  if (a.rows && a.q) f(std::true_type{}, std::true_type{});
-  else if (a.q) f(std::false_type{}, std::true_type{});
-  else f(std::true_type{}, std::false_type{});
+  using T = std::true_type;
+  using N = std::false_type;
+  const int past = past_caches(a);
+  auto go = [&](auto rows, auto codes) {
+    constexpr int kBoth = (decltype(rows)::value ? 1 : 0) | (decltype(codes)::value ? 2 : 0);
+    if ((past & kBoth) == kBoth) f(rows, codes, std::integral_constant<int, kBoth>{});
+    else if (kBoth == 3 && past == 1) f(rows, codes, std::integral_constant<int, kBoth & 1>{});
+    else f(rows, codes, std::integral_constant<int, 0>{});
+  };
+  if (a.rows && a.q) go(T{}, T{});
+  else if (a.q) go(N{}, T{});
+  else go(T{}, N{});
 }
 
 // Rows that cannot all stay in the 256 MiB cache in front of the memory are
@@ -332,14 +343,12 @@ hipError_t launch_moe_dispatch(const MoeRows& a, const void* x, int64_t ld_x, hi
   with_row(a.bf16, [&](auto row) {
     typedef decltype(row) Row;
     typedef typename Row::elem E;
-    with_outputs(a, [&](auto fr, auto fc) {
+    with_outputs(a, [&](auto fr, auto fc, auto past) {
       with_flag(h.wide, [&](auto wide) {
-        with_flag(aligned_out(a), [&](auto nt) {
-          hipLaunchKernelGGL((k_dispatch<Row, fr.value, fc.value, wide.value, nt.value>), dim3(grid),
-                             dim3(h.threads), 0, st, (const E*)x, ld_x, a.dst, (int)a.tokens, (int)a.k,
-                             (int)(a.tokens * a.k), (E*)a.rows, a.ld_rows, a.q, a.ld_q, a.s, a.ld_s, (int)a.cols,
-                             per_token);
-        });
+        hipLaunchKernelGGL((k_dispatch<Row, fr.value, fc.value, wide.value, past.value>), dim3(grid),
+                           dim3(h.threads), 0, st, (const E*)x, ld_x, a.dst, (int)a.tokens, (int)a.k,
+                           (int)(a.tokens * a.k), (E*)a.rows, a.ld_rows, a.q, a.ld_q, a.s, a.ld_s, (int)a.cols,
+                           per_token);
       });
     });
   });
@@ -373,15 +382,13 @@ hipError_t launch_moe_combine_bwd(const MoeRows& a, const void* dy, int64_t ld_d
   with_row(a.bf16, [&](auto row) {
     typedef decltype(row) Row;
     typedef typename Row::elem E;
-    with_outputs(a, [&](auto fr, auto fc) {
+    with_outputs(a, [&](auto fr, auto fc, auto past) {
       with_flag(h.wide, [&](auto wide) {
-        with_flag(aligned_out(a), [&](auto nt) {
-          with_flag(streamed(a), [&](auto nti) {
-            hipLaunchKernelGGL((k_combine_bwd<Row, fr.value, fc.value, wide.value, nt.value, nti.value>), dim3(grid),
-                               dim3(h.threads), 0, st, (const E*)dy, ld_dy, (const E*)yp, ld_yp, a.dst, w,
-                               (int)a.tokens, (int)a.k, (int)(a.tokens * a.k), (E*)a.rows, a.ld_rows, a.q, a.ld_q,
-                               a.s, a.ld_s, dw, (int)a.cols);
-          });
+        with_flag(streamed(a), [&](auto nti) {
+          hipLaunchKernelGGL((k_combine_bwd<Row, fr.value, fc.value, wide.value, past.value, nti.value>), dim3(grid),
+                             dim3(h.threads), 0, st, (const E*)dy, ld_dy, (const E*)yp, ld_yp, a.dst, w,
+                             (int)a.tokens, (int)a.k, (int)(a.tokens * a.k), (E*)a.rows, a.ld_rows, a.q, a.ld_q,
+                             a.s, a.ld_s, dw, (int)a.cols);
         });
       });
     });
