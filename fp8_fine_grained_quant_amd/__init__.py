@@ -893,7 +893,10 @@ _ROWS, _CODES = 1, 2
 
 
 def moe_dispatch(x, dst, stream=None):
-    """Token rows into expert order (zeros for dropped pairs)."""
+    """Token rows into expert order (zeros for dropped pairs).  Rows and codes
+    made here and by the calls below start on 64-byte segments, as the
+    quantizers and grouped products take them: where the columns do not fill
+    those, the result is a view with a larger row stride."""
     return _native().moe_dispatch(x, dst, None, None, None, _ROWS, stream)[0]
 
 

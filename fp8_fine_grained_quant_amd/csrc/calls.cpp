@@ -365,13 +365,21 @@ struct RowOutputs {
       expect(scale, {m, (cols + 127) / 128}, at::kFloat, "scale");
     }
   }
-  // Codes in rows that are a multiple of 16 bytes apart, as the grouped
-  // products take them.
+  // Rows and codes in rows a multiple of 64 bytes apart: the quantizers and the
+  // grouped products take them as they are, and they are written in whole
+  // segments.
+  static Tensor spaced(int64_t m, int64_t cols, int64_t bytes, ScalarType type, const Tensor& like) {
+    const int64_t step = 64 / bytes, ld = (cols + step - 1) / step * step;
+    const Tensor t = make({m, ld}, type, like);
+    return ld == cols ? t : t.narrow(1, 0, cols);
+  }
   void allocate(int want, int64_t m, int64_t cols, const Tensor& like) {
-    if (want & 1) rows = &given_or(nullptr, own_rows, {m, cols}, like.scalar_type(), like);
+    if (want & 1) {
+      own_rows = spaced(m, cols, (int64_t)like.element_size(), like.scalar_type(), like);
+      rows = &own_rows;
+    }
     if (want & 2) {
-      own_q = make({m, (cols + 15) / 16 * 16}, at::kByte, like);
-      if (own_q.size(1) != cols) own_q = own_q.narrow(1, 0, cols);
+      own_q = spaced(m, cols, 1, at::kByte, like);
       q = &own_q;
       scale = &given_or(nullptr, own_scale, {m, (cols + 127) / 128}, at::kFloat, like);
     }

@@ -52,6 +52,14 @@ __device__ __forceinline__ void place(int per_token, int& t, int& piece) {
   }
 }
 
+// The end of the last whole 64-byte segment of a row (of a code row where only
+// codes leave).  Kernels that store past the caches leave the waves that hold
+// the columns after it to plain stores.
+template <class Row, bool ROWS>
+__device__ __forceinline__ int whole_end(int cols) {
+  return cols & ~(ROWS ? 64 / (int)sizeof(typename Row::elem) - 1 : 63);
+}
+
 // First column of a piece.
 template <class Row>
 __device__ __forceinline__ int piece_col(int piece) { return (piece >> 4) * 128 + (piece & 15) * Row::kLen; }
@@ -106,7 +114,7 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_dispatch(
       }
     }
   };
-  if (no_cut<Row>(c0, cols)) body(std::true_type{}); else body(std::false_type{});
+  if (no_cut<Row>(c0, whole_end<Row, ROWS>(cols), cols)) body(std::true_type{}); else body(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------
@@ -150,7 +158,7 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_gather(
     }
     store_piece<Row, kWhole, 0>(y + (int64_t)t * ld_y, c0, cols, Row::pack(acc));
   };
-  if (no_cut<Row>(c0, cols)) body(std::true_type{}); else body(std::false_type{});
+  if (no_cut<Row>(c0, cols, cols)) body(std::true_type{}); else body(std::false_type{});
 }
 
 // ---------------------------------------------------------------------------
@@ -240,7 +248,8 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
       }
     };
     for (int piece = piece0; (piece >> 4) * 128 < cols; piece += step) {
-      if (no_cut<Row>(piece_col<Row>(piece), cols)) body(std::true_type{}, piece); else body(std::false_type{}, piece);
+      if (no_cut<Row>(piece_col<Row>(piece), whole_end<Row, ROWS>(cols), cols)) body(std::true_type{}, piece);
+      else body(std::false_type{}, piece);
     }
     const int nj = min(kJ, k - j0);
 #pragma unroll
@@ -290,16 +299,18 @@ Shape shape_of(int64_t cols) {
 }
 
 // Which outputs are stored past the caches (1: rows, 2: codes): those whose
-// rows start and end on whole 64-byte segments.  The combine gradient of 32768
-// rows of 7168 takes 246 us so and 271 us through the caches, the dispatch to
-// 16384 rows 69 and 81.  Cut segments lose by it: codes of 864 columns 35 us so
-// and 31 through the caches, of 832 columns 24 and 30; rows of 2047 BF16
-// columns 30 and 21.
+// rows start on 64-byte segments, up to the last whole one; codes beside rows
+// only where they fill theirs.  The combine gradient of 32768 rows of 7168
+// takes 246 us so and 271 us through the caches, the dispatch to 16384 rows 69
+// and 81.  Cut segments lose by it: 65000 rows of 864 columns with codes 43 us
+// with the codes past the caches, 30 with the rows alone; dense rows of 2047
+// BF16 columns 30 us past, 21 through.
 int past_caches(const MoeRows& a) {
   auto whole = [](const void* p, int64_t row_bytes) {
     return p && reinterpret_cast<uintptr_t>(p) % 64 == 0 && row_bytes % 64 == 0;
   };
-  return (whole(a.rows, a.ld_rows * (a.bf16 ? 2 : 4)) ? 1 : 0) | (whole(a.q, a.ld_q) ? 2 : 0);
+  return (whole(a.rows, a.ld_rows * (a.bf16 ? 2 : 4)) ? 1 : 0) |
+         (whole(a.q, a.ld_q) && (!a.rows || a.cols % 64 == 0) ? 2 : 0);
 }
 
 template <class F>

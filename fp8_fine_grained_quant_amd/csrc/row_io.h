@@ -104,16 +104,18 @@ struct RowF32 {
   __device__ __forceinline__ static void store1(elem* p, float v) { *p = v; }
 };
 
-// True if no lane of the wave has a run that the row's end cuts: then its runs
-// are inside or outside as a whole.  The branch on it is uniform, so loads and
-// stores inside carry no masks of single columns.
+// True if no lane of the wave has a run that column `end` cuts or that lies
+// between it and the row's end; end is the row's end, or that of its last whole
+// 64 columns.  Then the wave's runs are inside or outside as a whole.  The
+// branch on it is uniform, so loads and stores inside carry no masks of single
+// columns.
 template <class Row>
-__device__ __forceinline__ bool no_cut(int c0, int cols) {
+__device__ __forceinline__ bool no_cut(int c0, int end, int cols) {
   bool ok = true;
 #pragma unroll
   for (int r = 0; r < Row::kRuns; ++r) {
     const int cr = c0 + 64 * r;
-    ok = ok && (cr + Row::kLen <= cols || cr >= cols);
+    ok = ok && (cr + Row::kLen <= end || cr >= cols);
   }
   return __all(ok);
 }
@@ -171,13 +173,14 @@ __device__ __forceinline__ void store_bytes(void* to, u32x4 v, int n) {
   if (n & 2) *reinterpret_cast<u16_u*>(p) = (uint16_t)v[0];
 }
 
+// NT: past the caches, for whole pieces only.
 template <class Row, bool WHOLE, int NT>
 __device__ __forceinline__ void store_piece(typename Row::elem* p, int c0, int cols, const typename Row::Raw& raw) {
 #pragma unroll
   for (int r = 0; r < Row::kRuns; ++r) {
     const int cr = c0 + 64 * r;
     if (WHOLE ? cr < cols : cr + Row::kLen <= cols)
-      st16u<NT>(p + cr, raw.a[r]);
+      st16u<WHOLE && NT>(p + cr, raw.a[r]);
     else if (!WHOLE && cr < cols)
       store_bytes(p + cr, raw.a[r], (cols - cr) * (int)sizeof(typename Row::elem));
   }
@@ -191,8 +194,8 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int c0, int cols, uint32
     const int cr = c0 + 64 * r;
     uint32_t w = r == 0 ? w0 : w1;
     if (WHOLE ? cr < cols : cr + Row::kLen <= cols) {
-      if (Row::kRuns == 1) st8u<NT>(p + cr, u32x2{w0, w1});
-      else st4u<NT>(p + cr, w);
+      if (Row::kRuns == 1) st8u<WHOLE && NT>(p + cr, u32x2{w0, w1});
+      else st4u<WHOLE && NT>(p + cr, w);
     } else if (!WHOLE && cr < cols) {
       const int n = cols - cr;
       uint8_t* q = p + cr;

@@ -107,3 +107,19 @@ def test_missing_build_is_named(tmp_path):
             "try:\n    fq.moe_sort(torch.zeros(2, 2, dtype=torch.int32), 4)\n"
             "except RuntimeError as e:\n    assert 'not built' in str(e), e\nelse:\n    raise SystemExit(1)\n")
     assert subprocess.run([sys.executable, "-c", code]).returncode == 0
+
+
+@pytest.mark.gpu
+def test_made_rows_start_on_segments():
+    """Rows and codes of any width feed the quantizers and the grouped products
+    as they are (dense rows of 200 BF16 columns start off 16 bytes)."""
+    x = torch.randn(300, 200, device="cuda").to(bf16)
+    offsets, dst, _ = fq.moe_sort(torch.randint(0, 4, (300, 2), device="cuda").to(i32), 4)
+    rows, q, s = fq.moe_dispatch_quant(x, dst)
+    assert rows.shape == (600, 200) and rows.stride() == (224, 1) and q.stride() == (256, 1)
+    q_t, _ = fq.quant_transpose_grouped(rows, offsets)
+    assert q_t.shape[0] == 200
+    assert fq.moe_dispatch(torch.randn(300, 256, device="cuda").to(bf16), dst).is_contiguous()
+    again, scale = torch.empty(600, 208, dtype=u8, device="cuda")[:, :200], torch.empty(600, 2, device="cuda")
+    fq.fp8q_quant_act_1x128(rows, again, scale)
+    assert torch.equal(again, q) and torch.equal(scale, s)
