@@ -11,6 +11,7 @@
 #include <atomic>
 #include <stdint.h>
 #ifdef FP8Q_DEBUG
+#include <new>
 #include <vector>
 #endif
 
@@ -640,15 +641,19 @@ fp8q_status check_codes(const uint8_t* q, int64_t ld_q, const float* s, int64_t 
 // do; the FP8Q_DEBUG build rejects one that is not a permutation of the rows.
 fp8q_status debug_check_dst(const int32_t* dst, int64_t m, hipStream_t stream) {
 #ifdef FP8Q_DEBUG
-  std::vector<int32_t> h((size_t)m);
-  if (hipMemcpyAsync(h.data(), dst, h.size() * sizeof(int32_t), hipMemcpyDeviceToHost, stream) != hipSuccess ||
-      hipStreamSynchronize(stream) != hipSuccess)
+  try {
+    std::vector<int32_t> h((size_t)m);
+    if (hipMemcpyAsync(h.data(), dst, h.size() * sizeof(int32_t), hipMemcpyDeviceToHost, stream) != hipSuccess ||
+        hipStreamSynchronize(stream) != hipSuccess)
+      return FP8Q_ERR_LAUNCH;
+    std::vector<bool> seen((size_t)m, false);
+    for (const int32_t d : h) {
+      const int64_t r = d >= 0 ? (int64_t)d : -1 - (int64_t)d;
+      if (r >= m || seen[(size_t)r]) return FP8Q_ERR_SHAPE;
+      seen[(size_t)r] = true;
+    }
+  } catch (const std::bad_alloc&) {  // no memory for the copy: nothing was checked
     return FP8Q_ERR_LAUNCH;
-  std::vector<bool> seen((size_t)m, false);
-  for (const int32_t d : h) {
-    const int64_t r = d >= 0 ? (int64_t)d : -1 - (int64_t)d;
-    if (r >= m || seen[(size_t)r]) return FP8Q_ERR_SHAPE;
-    seen[(size_t)r] = true;
   }
 #else
   (void)dst; (void)m; (void)stream;
