@@ -20,19 +20,18 @@ namespace fp8q {
 
 namespace {
 
-constexpr int kJ = 8;              // choices handled together: 8 row loads in flight per lane
+constexpr int kJ = 8;              // choices handled together: 8 row loads or stores in flight per lane
+constexpr int kPair = 2;           // and in the combine gradient
 constexpr int kWideThreads = 512;  // most threads of a block that works on one token
 
 __device__ __forceinline__ bool row_ok(int r, int m) { return (uint32_t)r < (uint32_t)m; }
 // The row of a map entry, kept or dropped.
 __device__ __forceinline__ int row_of(int d) { return d >= 0 ? d : -1 - d; }
 
-template <class F>
+template <int J, int I = 0, class F>
 __device__ __forceinline__ void each_choice(F f) {
-  f(std::integral_constant<int, 0>{}); f(std::integral_constant<int, 1>{});
-  f(std::integral_constant<int, 2>{}); f(std::integral_constant<int, 3>{});
-  f(std::integral_constant<int, 4>{}); f(std::integral_constant<int, 5>{});
-  f(std::integral_constant<int, 6>{}); f(std::integral_constant<int, 7>{});
+  f(std::integral_constant<int, I>{});
+  if constexpr (I + 1 < J) each_choice<J, I + 1>(f);
 }
 
 // 16 lanes handle a 128-column group of a row, 8 columns each.  WIDE rows (a
@@ -162,128 +161,137 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_gather(
 }
 
 // ---------------------------------------------------------------------------
-// Combine backward: a token's products with its rows are summed inside one
-// block (WIDE) or one 16-lane group, without atomics: the order is fixed.
+// Combine backward: two choices of one token to a block (WIDE) or a 16-lane
+// group, whose lanes' products are summed there, without atomics: the order is
+// fixed.  dy is read again by the token's other blocks, from the caches; all
+// choices in one block need three times the registers and instructions (32768
+// rows of 7168 226 us so, 228 with four and 245 with eight; 4905 FP32 rows of
+// 2411 with codes 17 us, with eight 29).
 template <class Row, bool ROWS, bool CODES, bool WIDE, int PAST, int NTI>
 __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
     const typename Row::elem* __restrict__ dy, int64_t ld_dy, const typename Row::elem* __restrict__ yp,
     int64_t ld_yp, const int* __restrict__ dst, const float* __restrict__ w, int tokens, int k, int m,
     typename Row::elem* __restrict__ rows, int64_t ld_r, uint8_t* __restrict__ q, int64_t ld_q,
-    float* __restrict__ s, int64_t ld_s, float* __restrict__ dw, int cols) {
-  __shared__ float red[kWideThreads / 64][kJ];
-  int t, piece0;
-  place<WIDE>(WIDE ? 1 : 16, t, piece0);
+    float* __restrict__ s, int64_t ld_s, float* __restrict__ dw, int cols, int parts) {
+  constexpr int J = kPair;
+  __shared__ float red[kWideThreads / 64][J];
+  uint32_t item = WIDE ? blockIdx.x : blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (WIDE) {
+    // A token's blocks are 8 apart, on one XCD, whose L2 then holds its dy:
+    // the last tokens, fewer than 8, keep theirs together.
+    const uint32_t eight = 8u * (uint32_t)parts, group = item / eight, at = item - group * eight;
+    if ((int)(group * 8) + 8 <= tokens) item = (group * 8 + (at & 7)) * (uint32_t)parts + (at >> 3);
+  }
+  const int t = (int)(item / (uint32_t)parts), j0 = (int)(item - (uint32_t)t * (uint32_t)parts) * J;
   if (!WIDE && t >= tokens) return;
-  const int step = WIDE ? (int)blockDim.x : 16;
+  const int piece0 = WIDE ? (int)threadIdx.x : (int)threadIdx.x & 15, step = WIDE ? (int)blockDim.x : 16;
   const int64_t p0 = (int64_t)t * k;
-  for (int j0 = 0; j0 < k; j0 += kJ) {
-    int d[kJ], r[kJ];  // a choice's map entry and row; m: no choice
-    float wj[kJ], acc[kJ];
+  int d[J], r[J];  // a choice's map entry and row; m: no choice
+  float wj[J], acc[J];
 #pragma unroll
-    for (int u = 0; u < kJ; ++u) {
-      const int64_t at = p0 + min(j0 + u, k - 1);
-      d[u] = dst[at];
-      r[u] = j0 + u < k ? row_of(d[u]) : m;
-      wj[u] = w[at];
-      acc[u] = 0.f;
-    }
-    const int mine = j0 + (int)(threadIdx.x & (kJ - 1));
-    const int my_r = CODES && mine < k ? row_of(dst[p0 + mine]) : m;
-    auto body = [&](auto whole, int piece) {
-      constexpr bool kWhole = decltype(whole)::value;
-      const int c = piece >> 4, c0 = piece_col<Row>(piece);
-      const typename Row::Raw graw = load_piece<Row, kWhole, !WIDE, NTI>(dy + (int64_t)t * ld_dy, c0, cols);
-      typename Row::Raw raw[kJ];
+  for (int u = 0; u < J; ++u) {
+    const int64_t at = p0 + min(j0 + u, k - 1);
+    d[u] = dst[at];
+    r[u] = j0 + u < k ? row_of(d[u]) : m;
+    wj[u] = w[at];
+    acc[u] = 0.f;
+  }
+  const int mine = j0 + (int)(threadIdx.x & (J - 1));
+  const int my_r = CODES && mine < k ? row_of(dst[p0 + mine]) : m;
+  auto body = [&](auto whole, int piece) {
+    constexpr bool kWhole = decltype(whole)::value;
+    const int c = piece >> 4, c0 = piece_col<Row>(piece);
+    const typename Row::Raw graw = load_piece<Row, kWhole, !WIDE, 0>(dy + (int64_t)t * ld_dy, c0, cols);
+    typename Row::Raw raw[J];
 #pragma unroll
-      for (int u = 0; u < kJ; ++u)
-        if (d[u] >= 0 && row_ok(r[u], m))
-          raw[u] = load_piece<Row, kWhole, !WIDE, NTI>(yp + (int64_t)r[u] * ld_yp, c0, cols);
-      bool in[Row::kRuns];
+    for (int u = 0; u < J; ++u)
+      if (d[u] >= 0 && row_ok(r[u], m))
+        raw[u] = load_piece<Row, kWhole, !WIDE, NTI>(yp + (int64_t)r[u] * ld_yp, c0, cols);
+    bool in[Row::kRuns];
 #pragma unroll
-      for (int i = 0; i < Row::kRuns; ++i) in[i] = !kWhole || c0 + 64 * i < cols;
-      float g[8];
-      Row::unpack(graw, g);
-      uint32_t am[kJ];
+    for (int i = 0; i < Row::kRuns; ++i) in[i] = !kWhole || c0 + 64 * i < cols;
+    float g[8];
+    Row::unpack(graw, g);
+    uint32_t am[J];
 #pragma unroll
-      for (int u = 0; u < kJ; ++u) {
-        am[u] = 0;
-        if (!row_ok(r[u], m)) continue;
-        float v[8];
-        if (d[u] >= 0) {
-          Row::unpack(raw[u], v);
+    for (int u = 0; u < J; ++u) {
+      am[u] = 0;
+      if (!row_ok(r[u], m)) continue;
+      float v[8];
+      if (d[u] >= 0) {
+        Row::unpack(raw[u], v);
 #pragma unroll
-          for (int i = 0; i < Row::kRuns; ++i) {
-            float part = acc[u];
+        for (int i = 0; i < Row::kRuns; ++i) {
+          float part = acc[u];
 #pragma unroll
-            for (int e = i * Row::kLen; e < (i + 1) * Row::kLen; ++e) part = __builtin_fmaf(g[e], v[e], part);
-            acc[u] = in[i] ? part : acc[u];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = g[e] * wj[u];
-          raw[u] = Row::pack(v);
-        } else {
-          raw[u] = typename Row::Raw{};
+          for (int e = i * Row::kLen; e < (i + 1) * Row::kLen; ++e) part = __builtin_fmaf(g[e], v[e], part);
+          acc[u] = in[i] ? part : acc[u];
         }
-        if (ROWS) store_piece<Row, kWhole, PAST & 1>(rows + (int64_t)r[u] * ld_r, c0, cols, raw[u]);
-        if (CODES) am[u] = row16_max_u32(Row::max_bits(raw[u]));  // the codes are those of the rounded row
-      }
-      if (CODES) {
-        // lane u of the group forms the scale of row u
-        const int lig = piece & 15;
-        uint32_t a = am[0];
 #pragma unroll
-        for (int u = 1; u < kJ; ++u) a = (lig & 7) == u ? +am[u] : a;
-        float sc, inv;
-        group_scale(__uint_as_float(a), sc, inv);
-        if (lig < kJ && row_ok(my_r, m)) s[(int64_t)my_r * ld_s + c] = sc;
-        each_choice([&](auto u) {
-          if (!row_ok(r[u.value], m)) return;
-          const float iu = row_bcast<u.value>(inv);
-          float v[8];
-          Row::unpack(raw[u.value], v);
-          store_codes<Row, kWhole, PAST / 2>(q + (int64_t)r[u.value] * ld_q, c0, cols,
-                                       pack4_e4m3_grp(v[0] * iu, v[1] * iu, v[2] * iu, v[3] * iu),
-                                       pack4_e4m3_grp(v[4] * iu, v[5] * iu, v[6] * iu, v[7] * iu));
-        });
+        for (int e = 0; e < 8; ++e) v[e] = g[e] * wj[u];
+        raw[u] = Row::pack(v);
+      } else {
+        raw[u] = typename Row::Raw{};
       }
-    };
-    for (int piece = piece0; (piece >> 4) * 128 < cols; piece += step) {
-      if (no_cut<Row>(piece_col<Row>(piece), whole_end<Row, ROWS>(cols), cols)) body(std::true_type{}, piece);
-      else body(std::false_type{}, piece);
+      if (ROWS) store_piece<Row, kWhole, PAST & 1>(rows + (int64_t)r[u] * ld_r, c0, cols, raw[u]);
+      if (CODES) am[u] = row16_max_u32(Row::max_bits(raw[u]));  // the codes are those of the rounded row
     }
-    const int nj = min(kJ, k - j0);
+    if (CODES) {
+      // lane u of the group forms the scale of row u
+      const int lig = piece & 15;
+      uint32_t a = am[0];
 #pragma unroll
-    for (int u = 0; u < kJ; ++u) acc[u] = row16_sum(acc[u]);
-    if (WIDE) {
-      const int lane = threadIdx.x & 63, waves = (int)blockDim.x >> 6;
-#pragma unroll
-      for (int u = 0; u < kJ; ++u) {
-        acc[u] += __shfl_xor(acc[u], 16);
-        acc[u] += __shfl_xor(acc[u], 32);
-      }
-      if (lane == 0)
-#pragma unroll
-        for (int u = 0; u < kJ; ++u) red[threadIdx.x >> 6][u] = acc[u];
-      __syncthreads();
-      if ((int)threadIdx.x < nj) {
-        float sum = 0.f;
-        for (int i = 0; i < waves; ++i) sum += red[i][threadIdx.x];
-        dw[p0 + j0 + threadIdx.x] = sum;
-      }
-      __syncthreads();
-    } else {
-#pragma unroll
-      for (int u = 0; u < kJ; ++u)
-        if ((threadIdx.x & 15) == u && u < nj) dw[p0 + j0 + u] = acc[u];
+      for (int u = 1; u < J; ++u) a = (lig & (J - 1)) == u ? +am[u] : a;
+      float sc, inv;
+      group_scale(__uint_as_float(a), sc, inv);
+      if (lig < J && row_ok(my_r, m)) s[(int64_t)my_r * ld_s + c] = sc;
+      each_choice<J>([&](auto u) {
+        if (!row_ok(r[u.value], m)) return;
+        const float iu = row_bcast<u.value>(inv);
+        float v[8];
+        Row::unpack(raw[u.value], v);
+        store_codes<Row, kWhole, PAST / 2>(q + (int64_t)r[u.value] * ld_q, c0, cols,
+                                     pack4_e4m3_grp(v[0] * iu, v[1] * iu, v[2] * iu, v[3] * iu),
+                                     pack4_e4m3_grp(v[4] * iu, v[5] * iu, v[6] * iu, v[7] * iu));
+      });
     }
+  };
+  for (int piece = piece0; (piece >> 4) * 128 < cols; piece += step) {
+    if (no_cut<Row>(piece_col<Row>(piece), whole_end<Row, ROWS>(cols), cols)) body(std::true_type{}, piece);
+    else body(std::false_type{}, piece);
+  }
+  const int nj = min(J, k - j0);
+#pragma unroll
+  for (int u = 0; u < J; ++u) acc[u] = row16_sum(acc[u]);
+  if (WIDE) {
+    const int lane = threadIdx.x & 63, waves = (int)blockDim.x >> 6;
+#pragma unroll
+    for (int u = 0; u < J; ++u) {
+      acc[u] += __shfl_xor(acc[u], 16);
+      acc[u] += __shfl_xor(acc[u], 32);
+    }
+    if (lane == 0)
+#pragma unroll
+      for (int u = 0; u < J; ++u) red[threadIdx.x >> 6][u] = acc[u];
+    __syncthreads();
+    if ((int)threadIdx.x < nj) {
+      float sum = 0.f;
+      for (int i = 0; i < waves; ++i) sum += red[i][threadIdx.x];
+      dw[p0 + j0 + threadIdx.x] = sum;
+    }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int u = 0; u < J; ++u)
+      if ((threadIdx.x & 15) == u && u < nj) dw[p0 + j0 + u] = acc[u];
   }
 }
 
 // Blocks of wide rows: the row's pieces in as few slices as blocks of
 // kWideThreads allow, of equal length up to a wave (7168 columns: two slices of
 // 448 threads, where slices of 512 would leave an eighth of the lanes idle).
-// The combine gradient of 32768 rows of 7168: 246 us so, 260 with blocks of
-// 128, 249 with 256 and 248 with 1024; the other kernels differ less.
+// The dispatch to 16384 rows of 7168: 69 us so, 73 with blocks of 256; the
+// other kernels differ less.
 struct Shape {
   bool wide;
   int slices, threads;
@@ -301,7 +309,7 @@ Shape shape_of(int64_t cols) {
 // Which outputs are stored past the caches (1: rows, 2: codes): those whose
 // rows start on 64-byte segments, up to the last whole one; codes beside rows
 // only where they fill theirs.  The combine gradient of 32768 rows of 7168
-// takes 246 us so and 271 us through the caches, the dispatch to 16384 rows 69
+// took 246 us so and 271 us through the caches, the dispatch to 16384 rows 69
 // and 81.  Cut segments lose by it: 65000 rows of 864 columns with codes 43 us
 // with the codes past the caches, 30 with the rows alone; dense rows of 2047
 // BF16 columns 30 us past, 21 through.
@@ -389,7 +397,8 @@ hipError_t launch_moe_gather(const MoeRows& a, const float* w, void* y, int64_t 
 hipError_t launch_moe_combine_bwd(const MoeRows& a, const void* dy, int64_t ld_dy, const void* yp, int64_t ld_yp,
                                   const float* w, float* dw, hipStream_t st) {
   const Shape h = shape_of(a.cols);
-  const uint32_t grid = (uint32_t)(h.wide ? a.tokens : (a.tokens + 15) / 16);
+  const int parts = (int)((a.k + kPair - 1) / kPair);
+  const uint32_t grid = (uint32_t)(h.wide ? a.tokens * parts : (a.tokens * parts + 15) / 16);
   with_row(a.bf16, [&](auto row) {
     typedef decltype(row) Row;
     typedef typename Row::elem E;
@@ -399,7 +408,7 @@ hipError_t launch_moe_combine_bwd(const MoeRows& a, const void* dy, int64_t ld_d
           hipLaunchKernelGGL((k_combine_bwd<Row, fr.value, fc.value, wide.value, past.value, nti.value>), dim3(grid),
                              dim3(h.threads), 0, st, (const E*)dy, ld_dy, (const E*)yp, ld_yp, a.dst, w,
                              (int)a.tokens, (int)a.k, (int)(a.tokens * a.k), (E*)a.rows, a.ld_rows, a.q, a.ld_q,
-                             a.s, a.ld_s, dw, (int)a.cols);
+                             a.s, a.ld_s, dw, (int)a.cols, parts);
         });
       });
     });
