@@ -134,14 +134,14 @@ __global__ __launch_bounds__(kClipThreads) void k_grad_scale(const ClipBatch* __
                                                              const double* __restrict__ part, int parts,
                                                              double max_norm, float* __restrict__ norm_out) {
   __shared__ double red[4];
-  const ClipBatch& b = *table;
   double s = 0;
   for (int i = threadIdx.x; i < parts; i += kClipThreads) s += part[i];
   const double norm = sqrt(block_sum(s, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   // a NaN norm fails the comparison and gives a NaN factor, an infinite one 0
   const float f = norm <= max_norm ? 1.f : (float)(max_norm / norm);
-  if (chunks == 0) return;  // no table
+  if (chunks == 0) return;  // no table, and a null pointer to it: no reference before this
+  const ClipBatch& b = *table;
   const ClipFinder<kMaxClipTensors> find(b);
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     int64_t lo;
