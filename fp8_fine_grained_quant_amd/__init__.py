@@ -792,9 +792,12 @@ def _bind(lib):
 
 
 def _on_stream(name, args, stream):
-    """The native call `name` with `stream` as torch's current stream."""
-    side = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(side):
+    """The native call `name` with `stream` as torch's current stream.  The
+    address 0 is the default stream; as that of an external stream torch takes
+    it for none given, and hands out a stream of its pool."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
         return getattr(_bound, name)(*args, None)
 
 
