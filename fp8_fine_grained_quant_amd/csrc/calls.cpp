@@ -170,11 +170,12 @@ hipStream_t handle_of(PyObject* o) {
   if (!p && PyErr_Occurred()) throw python_error();
   return static_cast<hipStream_t>(p);
 }
-// None, a torch stream or a pointer as a number.
+// None, a torch stream or a pointer as a number of any kind.
 hipStream_t stream_of(PyObject* o) {
   if (o != Py_None) {
     if (PyLong_Check(o)) return handle_of(o);
-    THPObjectPtr handle(PyObject_GetAttrString(o, "cuda_stream"));
+    THPObjectPtr handle(PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream")
+                                                                 : PyNumber_Long(o));
     if (!handle) throw python_error();
     return handle_of(handle.get());
   }

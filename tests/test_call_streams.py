@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import fp8_fine_grained_quant_amd as fq
+from fake_device import NO_MEMORY, current_device, hollow
 
 
 class Recorder:
@@ -93,3 +94,43 @@ def test_order_on_the_stream(name):
     torch.cuda.synchronize()
     for i, (a, b) in enumerate(zip(read, want)):
         assert torch.equal(a, b), i
+
+
+class Address:
+    def __init__(self, p):
+        self.p = p
+
+    def __int__(self):
+        return self.p
+
+
+@pytest.mark.parametrize("stream", [None, 0, 64, np.int64(0), np.uint64(64), Address(64)], ids=lambda s: type(s).__name__)
+def test_kinds_of_numbers(stream):
+    """Taken with given outputs: the call goes on to the tensors' memory."""
+    x, ids, w = hollow(6, 32), hollow(6, 4, dt=torch.int32), hollow(6, 4)
+    with current_device(0), pytest.raises(RuntimeError, match=NO_MEMORY):
+        fq.fp8q_moe_route(x, ids, w, stream=stream)
+
+
+def test_no_stream():
+    x, ids, w = hollow(6, 32), hollow(6, 4, dt=torch.int32), hollow(6, 4)
+    for bad, error in ((1 << 80, OverflowError), (object(), TypeError), ("now", ValueError)):
+        with current_device(0), pytest.raises(error):
+            fq.fp8q_moe_route(x, ids, w, stream=bad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [int, np.int64, Address])
+def test_numbers_on_the_gpu(kind):
+    """A stream's address as any number, with and without given outputs."""
+    logits = torch.randn(50, 32, device="cuda")
+    ids, w = fq.moe_route(logits, 4)
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.default_stream(), torch.cuda.Stream()):
+        made = fq.moe_route(logits, 4, stream=kind(stream.cuda_stream))
+        out = torch.empty_like(ids), torch.empty_like(w)
+        torch.cuda.synchronize()
+        fq.fp8q_moe_route(logits, *out, stream=kind(stream.cuda_stream))
+        torch.cuda.synchronize()
+        for got in (made, out):
+            assert torch.equal(got[0], ids) and torch.equal(got[1], w)
