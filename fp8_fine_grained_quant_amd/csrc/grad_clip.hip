@@ -3,8 +3,10 @@
 //   norm = sqrt(sum over all tensors of g^2),  out = g * min(1, max_norm / norm)
 //
 // Squares are formed and summed in 64 bits, so no finite gradient overflows or
-// vanishes and the norm does not depend on how the elements are spread over
-// threads beyond the last FP64 bits; the order of every sum is fixed.  Two
+// vanishes in the norm, and it does not depend on how the elements are spread
+// over threads beyond the last FP64 bits; the order of every sum is fixed.  The
+// factor and its products are in 64 bits as well (the times are the same with
+// FP32 products): the only rounding to fewer is the output's.  Two
 // passes over the data, since the factor needs the whole norm first; both are
 // bound by memory.  470M gradients (1.88 GB) to BF16: 773 us, 6.1 TB/s over the
 // 4.7 GB of both passes.  The second pass reads and writes past the caches
@@ -138,8 +140,10 @@ __global__ __launch_bounds__(kClipThreads) void k_grad_scale(const ClipBatch* __
   for (int i = threadIdx.x; i < parts; i += kClipThreads) s += part[i];
   const double norm = sqrt(block_sum(s, red));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  // a NaN norm fails the comparison and gives a NaN factor, an infinite one 0
-  const float f = norm <= max_norm ? 1.f : (float)(max_norm / norm);
+  // A NaN norm fails the comparison and gives a NaN factor, an infinite one 0.
+  // The factor may be far below FP32's range where its product with a gradient
+  // is not, so it and the product are in 64 bits.
+  const double f = norm <= max_norm ? 1.0 : max_norm / norm;
   if (chunks == 0) return;  // no table, and a null pointer to it: no reference before this
   const ClipBatch& b = *table;
   const ClipFinder<kMaxClipTensors> find(b);
@@ -147,14 +151,14 @@ __global__ __launch_bounds__(kClipThreads) void k_grad_scale(const ClipBatch* __
     int64_t lo;
     int len;
     const int i = find(c, lo, len);
-    if (!OUT_BF16 && f == 1.f && b.out[i] == b.g[i]) continue;  // in place, and nothing to clip
+    if (!OUT_BF16 && f == 1.0 && b.out[i] == b.g[i]) continue;  // in place, and nothing to clip
     float v[kClipLoads][4];
     load_chunk<1>(b.g[i] + lo, len, v);
 #pragma unroll
     for (int l = 0; l < kClipLoads; ++l) {
       const int e = l * kClipStep + (int)threadIdx.x * 4;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[l][j] *= f;
+      for (int j = 0; j < 4; ++j) v[l][j] = (float)((double)v[l][j] * f);
       store_clipped<OUT_BF16, 1>(b.out[i], lo + e, v[l], len - e);
     }
   }

@@ -621,13 +621,15 @@ fp8q_status fp8q_moe_combine_bwd(const void* dy, const void* yp, fp8q_dtype t, i
 /*
  * Gradient clipping by the global norm: norm = sqrt(sum of g^2 over all
  * tensors), formed in 64 bits, and out = g * c, c = 1 if norm <= max_norm, else
- * max_norm / norm (so a NaN norm gives NaN, an infinite one zeros and NaN).
+ * max_norm / norm (so a NaN norm gives NaN, an infinite one zeros and NaN); c
+ * and the product are in 64 bits too, rounded to FP32 and then to out's type.
  *   grads : HOST array (read during the call only) of n dense FP32 tensors of
  *           any length; out is of type ot, and may be g itself if ot is FP32
  *           (then nothing is written where c = 1)
  *   max_norm : >= 0; +inf only measures and copies
  *   workspace : 8-byte aligned, fp8q_grad_clip_workspace(n) bytes
- *   norm  : one FP32, the norm before clipping
+ *   norm  : one FP32, the norm before clipping (infinite where FP32 cannot hold
+ *           it; the outputs are right there too)
  * n = 0 gives norm 0.  Tensors must not overlap each other.
  */
 typedef struct {
