@@ -38,6 +38,10 @@ grouped_gemm, quant_mx, quant_mx_transpose, gemm_mx, grouped_gemm_mx, grouped_ge
 backward and the dual-output quantizer); moe_route, moe_route_bwd, moe_sort,
 moe_dispatch, moe_dispatch_quant, moe_dispatch_bwd, moe_combine,
 moe_combine_bwd, moe_combine_bwd_quant, grad_clip.
+
+The MoE routing and clipping calls take tensors of the current device (a
+stream object given to a call that allocates makes its device the current one)
+and refuse others.
 """
 
 import ctypes

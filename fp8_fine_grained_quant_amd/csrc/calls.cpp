@@ -131,9 +131,18 @@ fp8q_dtype type_of(const Tensor& t) {
   refuse(PyExc_TypeError, "unsupported dtype " + name_of(t.scalar_type()));
 }
 
-void on_gpu(std::initializer_list<const Tensor*> ts) {
+[[noreturn]] void refuse_place() { refuse(PyExc_ValueError, "fp8q works on GPU tensors only"); }
+[[noreturn]] void refuse_devices(c10::Device a, c10::Device b) {
+  refuse(PyExc_ValueError, "tensors on " + a.str() + " and " + b.str() + ", expected one device");
+}
+// Tensors on one GPU, which is the result.
+c10::Device on_gpu(std::initializer_list<const Tensor*> ts) {
   for (const Tensor* t : ts)
-    if (t && !t->is_cuda()) refuse(PyExc_ValueError, "fp8q works on GPU tensors only");
+    if (t && !t->is_cuda()) refuse_place();
+  const c10::Device device = (*ts.begin())->device();
+  for (const Tensor* t : ts)
+    if (t && t->device() != device) refuse_devices(device, t->device());
+  return device;
 }
 void dense(std::initializer_list<const Tensor*> ts) {
   for (const Tensor* t : ts)
@@ -170,8 +179,15 @@ hipStream_t handle_of(PyObject* o) {
   if (!p && PyErr_Occurred()) throw python_error();
   return static_cast<hipStream_t>(p);
 }
-// None, a torch stream or a pointer as a number of any kind.
-hipStream_t stream_of(PyObject* o) {
+// The stream to launch on, given as None, a torch stream or a pointer as a
+// number of any kind.  A launch is on the current device, which must be the
+// tensors' own (index -1: there are none).
+hipStream_t stream_of(PyObject* o, c10::Device device) {
+  THPObjectPtr current(PyObject_CallNoArgs(current_device));
+  if (!current) throw python_error();
+  if (const int64_t at = integer(current.get()); device.index() >= 0 && at != device.index())
+    refuse(PyExc_ValueError,
+           "tensors on " + device.str() + ", but the current device is cuda:" + std::to_string(at));
   if (o != Py_None) {
     if (PyLong_Check(o)) return handle_of(o);
     THPObjectPtr handle(PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream")
@@ -179,9 +195,7 @@ hipStream_t stream_of(PyObject* o) {
     if (!handle) throw python_error();
     return handle_of(handle.get());
   }
-  THPObjectPtr device(PyObject_CallNoArgs(current_device));
-  if (!device) throw python_error();
-  THPObjectPtr handle(PyObject_CallFunctionObjArgs(current_stream, device.get(), nullptr));
+  THPObjectPtr handle(PyObject_CallFunctionObjArgs(current_stream, current.get(), nullptr));
   if (!handle) throw python_error();
   return handle_of(handle.get());
 }
@@ -259,7 +273,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     expect(weights, {tokens, k}, at::kFloat, "weights");
   }
   if (bias) expect(bias, {experts}, at::kFloat, "bias");
-  on_gpu({&logits, ids, weights, bias});
+  const c10::Device device = on_gpu({&logits, ids, weights, bias});
   dense({ids, weights, bias});
   const fp8q_dtype type = type_of(logits);
   const int64_t ld = stride(logits);
@@ -267,7 +281,7 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor own_ids, own_weights;
   const Tensor& i = given_or(ids, own_ids, {tokens, k}, at::kInt, logits);
   const Tensor& w = given_or(weights, own_weights, {tokens, k}, at::kFloat, logits);
-  const hipStream_t st = stream_of(a[8]);
+  const hipStream_t st = stream_of(a[8], device);
   check(unlocked([&] {
           return lib.moe_route(data<void>(logits), type, tokens, experts, ld, k, score, data<float>(bias), renorm,
                                scale, data<int32_t>(i), data<float>(w), st);
@@ -293,13 +307,13 @@ PyObject* moe_route_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int k = (int)std::min<int64_t>(ids.size(1), std::numeric_limits<int>::max());
   expect(&dweights, {tokens, k}, at::kFloat, "dweights");
   if (dlogits) expect(dlogits, {tokens, experts}, logits.scalar_type(), "dlogits");
-  on_gpu({&dweights, &logits, &ids, dlogits});
+  const c10::Device device = on_gpu({&dweights, &logits, &ids, dlogits});
   dense({&dweights, &ids});
   const fp8q_dtype type = type_of(logits);
   Tensor own;
   const Tensor& d = given_or(dlogits, own, {tokens, experts}, logits.scalar_type(), logits);
   const int64_t ld = stride(logits), ld_d = stride(d);
-  const hipStream_t st = stream_of(a[7]);
+  const hipStream_t st = stream_of(a[7], device);
   check(unlocked([&] {
           return lib.moe_route_bwd(data<float>(dweights), data<void>(logits), type, tokens, experts, ld,
                                    data<int32_t>(ids), k, score, renorm, scale, data<void>(d), ld_d, st);
@@ -326,7 +340,7 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (src) expect(src, {pairs}, at::kInt, "src");
     if (ws) expect(ws, {-1}, at::kByte, "workspace");
   }
-  on_gpu({&ids, offsets, dst, src, ws});
+  const c10::Device device = on_gpu({&ids, offsets, dst, src, ws});
   dense({&ids, offsets, dst, src, ws});
   const int cover = truth(a[2]);
   Tensor own_offsets, own_dst, own_src, own_ws;
@@ -340,7 +354,7 @@ PyObject* moe_sort(PyObject*, PyObject* const* a, Py_ssize_t n) {
     src = &given_or(nullptr, own_src, {pairs}, at::kInt, ids);
     if (need) ws = &given_or(nullptr, own_ws, {need}, at::kByte, ids);
   }
-  const hipStream_t st = stream_of(a[7]);
+  const hipStream_t st = stream_of(a[7], device);
   check(unlocked([&] {
           return lib.moe_sort(data<int32_t>(ids), pairs, experts, cover, data<int32_t>(offsets), data<int32_t>(dst),
                               data<int32_t>(src), data<void>(ws), ws ? ws->numel() : 0, st);
@@ -403,12 +417,12 @@ PyObject* moe_dispatch(PyObject*, PyObject* const* a, Py_ssize_t n) {
   expect_map(dst, tokens, "dst");
   const int64_t k = dst.size(1), m = tokens * k;
   out.expect_all(m, cols, x.scalar_type());
-  on_gpu({&x, &dst, out.rows, out.q, out.scale});
+  const c10::Device device = on_gpu({&x, &dst, out.rows, out.q, out.scale});
   dense({&dst});
   const fp8q_dtype type = type_of(x);
   if (a[5] != Py_None) out.allocate(small(a[5]), m, cols, x);
   const int64_t ld = stride(x), ld_r = out.ld_rows(), ld_q = out.ld_q(), ld_s = out.ld_scale();
-  const hipStream_t st = stream_of(a[6]);
+  const hipStream_t st = stream_of(a[6], device);
   check(unlocked([&] {
           return lib.moe_dispatch(data<void>(x), type, tokens, cols, ld, data<int32_t>(dst), (int)k,
                                   data<void>(out.rows), ld_r, data<uint8_t>(out.q), ld_q, data<float>(out.scale),
@@ -432,13 +446,13 @@ PyObject* moe_dispatch_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t tokens = dst.size(0), k = dst.size(1), cols = drows.size(1);
   expect(&drows, {tokens * k, cols}, drows.scalar_type(), "drows");
   if (dx) expect(dx, {tokens, cols}, drows.scalar_type(), "dx");
-  on_gpu({&drows, &dst, dx});
+  const c10::Device device = on_gpu({&drows, &dst, dx});
   dense({&dst});
   const fp8q_dtype type = type_of(drows);
   Tensor own;
   const Tensor& y = given_or(dx, own, {tokens, cols}, drows.scalar_type(), drows);
   const int64_t ld = stride(drows), ld_y = stride(y);
-  const hipStream_t st = stream_of(a[3]);
+  const hipStream_t st = stream_of(a[3], device);
   check(unlocked([&] {
           return lib.moe_dispatch_bwd(data<void>(drows), type, tokens, cols, ld, data<int32_t>(dst), (int)k,
                                       data<void>(y), ld_y, st);
@@ -461,13 +475,13 @@ PyObject* moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   expect(&yp, {tokens * k, cols}, yp.scalar_type(), "yp");
   expect(&weights, {tokens, k}, at::kFloat, "weights");
   if (out) expect(out, {tokens, cols}, yp.scalar_type(), "y");
-  on_gpu({&yp, &dst, &weights, out});
+  const c10::Device device = on_gpu({&yp, &dst, &weights, out});
   dense({&dst, &weights});
   const fp8q_dtype type = type_of(yp);
   Tensor own;
   const Tensor& y = given_or(out, own, {tokens, cols}, yp.scalar_type(), yp);
   const int64_t ld = stride(yp), ld_y = stride(y);
-  const hipStream_t st = stream_of(a[4]);
+  const hipStream_t st = stream_of(a[4], device);
   check(unlocked([&] {
           return lib.moe_combine(data<void>(yp), type, tokens, cols, ld, data<int32_t>(dst), (int)k,
                                  data<float>(weights), data<void>(y), ld_y, st);
@@ -495,14 +509,14 @@ PyObject* moe_combine_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   expect(&weights, {tokens, k}, at::kFloat, "weights");
   if (dweights) expect(dweights, {tokens, k}, at::kFloat, "dweights");
   out.expect_all(m, cols, dy.scalar_type());
-  on_gpu({&dy, &yp, &dst, &weights, dweights, out.rows, out.q, out.scale});
+  const c10::Device device = on_gpu({&dy, &yp, &dst, &weights, dweights, out.rows, out.q, out.scale});
   dense({&dst, &weights, dweights});
   const fp8q_dtype type = type_of(dy);
   if (!dweights) out.allocate(small(a[8]), m, cols, dy);
   Tensor own;
   const Tensor& dw = given_or(dweights, own, {tokens, k}, at::kFloat, dy);
   const int64_t ld = stride(dy), ld_p = stride(yp), ld_r = out.ld_rows(), ld_q = out.ld_q(), ld_s = out.ld_scale();
-  const hipStream_t st = stream_of(a[9]);
+  const hipStream_t st = stream_of(a[9], device);
   check(unlocked([&] {
           return lib.moe_combine_bwd(data<void>(dy), data<void>(yp), type, tokens, cols, ld, ld_p, data<int32_t>(dst),
                                      (int)k, data<float>(weights), data<void>(out.rows), ld_r, data<uint8_t>(out.q),
@@ -521,22 +535,27 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 6);
   if (a[3] == Py_None && a[n - 1] != Py_None) return again_on("grad_clip", a, n);
-  THPObjectPtr grads(PySequence_Fast(a[0], "grads: expected a sequence of tensors"));
-  if (!grads) throw python_error();
-  THPObjectPtr outs(PySequence_Fast(a[1] == Py_None ? grads.get() : a[1], "out: expected a sequence of tensors"));
-  if (!outs) throw python_error();
-  const Py_ssize_t tensors = PySequence_Fast_GET_SIZE(grads.get());
-  if (PySequence_Fast_GET_SIZE(outs.get()) != tensors)
-    refuse(PyExc_ValueError, "out: " + std::to_string(PySequence_Fast_GET_SIZE(outs.get())) + " tensors for " +
+  // tuples of the caller's lists, which other code may change before the launch
+  auto fixed = [](PyObject* o, const char* text) {
+    THPObjectPtr items(PySequence_Fast(o, text));
+    THPObjectPtr t(items ? PySequence_Tuple(items.get()) : nullptr);
+    if (!t) throw python_error();
+    return t;
+  };
+  THPObjectPtr grads = fixed(a[0], "grads: expected a sequence of tensors");
+  THPObjectPtr outs = fixed(a[1] == Py_None ? grads.get() : a[1], "out: expected a sequence of tensors");
+  const Py_ssize_t tensors = PyTuple_GET_SIZE(grads.get());
+  if (PyTuple_GET_SIZE(outs.get()) != tensors)
+    refuse(PyExc_ValueError, "out: " + std::to_string(PyTuple_GET_SIZE(outs.get())) + " tensors for " +
                                  std::to_string(tensors) + " gradients");
   const Tensor *norm = optional(a[3], "norm"), *ws = optional(a[4], "workspace");
-  std::vector<fp8q_grad> table((size_t)tensors);
   ScalarType type = at::kFloat;
+  const Tensor* abroad = nullptr;
   bool gpu = true;
   c10::Device device(c10::kCUDA);
   for (Py_ssize_t i = 0; i < tensors; ++i) {
-    const Tensor &g = tensor(PySequence_Fast_GET_ITEM(grads.get(), i), "grads"),
-                 &o = tensor(PySequence_Fast_GET_ITEM(outs.get(), i), "out");
+    const Tensor &g = tensor(PyTuple_GET_ITEM(grads.get(), i), "grads"),
+                 &o = tensor(PyTuple_GET_ITEM(outs.get(), i), "out");
     if (i == 0) {
       type = o.scalar_type();
       device = g.device();
@@ -549,15 +568,19 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!g.is_contiguous() || !o.is_contiguous())
       refuse(PyExc_ValueError, "gradients and their outputs must be contiguous");
     gpu = gpu && g.is_cuda() && o.is_cuda();
-    table[(size_t)i] = {data<float>(g), data<void>(o), g.numel()};
+    if (g.device() != device) abroad = &g;
+    if (o.device() != device) abroad = &o;
   }
   if (norm) {
     expect(norm, {}, at::kFloat, "norm");
     expect(ws, {-1}, at::kByte, "workspace");
     dense({ws});
+    const c10::Device at = on_gpu({norm, ws});
+    if (tensors == 0) device = at;
+    if (gpu && at != device) refuse_devices(device, at);
   }
-  on_gpu({norm, ws});
-  if (!gpu) refuse(PyExc_ValueError, "fp8q works on GPU tensors only");
+  if (!gpu) refuse_place();
+  if (abroad) refuse_devices(device, abroad->device());
   if (type != at::kFloat && type != at::kBFloat16) refuse(PyExc_TypeError, "unsupported dtype " + name_of(type));
   const double max_norm = real(a[2]);
   Tensor own_norm, own_ws;
@@ -567,7 +590,13 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
     norm = &own_norm;
     ws = &own_ws;
   }
-  const hipStream_t st = stream_of(a[5]);
+  const hipStream_t st = stream_of(a[5], device);
+  std::vector<fp8q_grad> table((size_t)tensors);
+  for (Py_ssize_t i = 0; i < tensors; ++i) {
+    const Tensor& g = THPVariable_Unpack(PyTuple_GET_ITEM(grads.get(), i));
+    table[(size_t)i] = {data<float>(g), data<void>(THPVariable_Unpack(PyTuple_GET_ITEM(outs.get(), i))),
+                        g.numel()};
+  }
   check(unlocked([&] {
           return lib.grad_clip(table.data(), tensors, type == at::kBFloat16 ? FP8Q_BF16 : FP8Q_F32, max_norm,
                                data<void>(ws), ws->numel(), data<float>(norm), st);
