@@ -622,7 +622,9 @@ fp8q_status check_route(fp8q_dtype lt, int64_t T, int64_t E, int k, int score, i
 }
 
 // The sizes of the row entry points: columns, groups and 8-column pieces are
-// counted in 32 bits, past a row's end too.
+// counted in 32 bits, past a row's end too.  A launch with a thread for each
+// piece of a token's columns has at most 1.6 times as many threads, below 2^32;
+// those with more go in parts.
 fp8q_status check_moe_rows(fp8q_dtype t, int64_t T, int64_t H, int k) {
   if (!valid_dtype(t)) return FP8Q_ERR_DTYPE;
   if (T < 0 || H < 0 || T > kMaxDim || H > kMaxDim || k < 1 || k > fp8q::kMaxTopK || T * k > kMaxDim)

@@ -127,6 +127,18 @@ struct MxArgs {
 hipError_t launch_gemm_mx(const MxArgs& a, hipStream_t st);
 
 // ------------------------------------------------------------ MoE routing
+// launch(first, count) for all tokens, a part of them at a time: a grid's threads
+// are counted in 32 bits, and 2^26 tokens of 64 threads each are past that.
+template <class F>
+hipError_t launch_in_parts(int64_t tokens, int64_t threads_per_token, F launch) {
+  const int64_t most = ((int64_t)1 << 31) / threads_per_token;
+  for (int64_t t = 0; t < tokens; t += most) {
+    launch(t, tokens - t < most ? tokens - t : most);
+    if (const hipError_t err = hipGetLastError(); err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
 constexpr int kMaxExperts = 1024;  // router and sort (their tables live in LDS)
 constexpr int kMaxTopK = 32;       // choices per token
 

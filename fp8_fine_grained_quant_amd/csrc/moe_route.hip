@@ -676,14 +676,17 @@ dim3 route_grid(int64_t tokens, int lanes) {
 }  // namespace
 
 hipError_t launch_moe_route(const MoeRoute& a, const float* bias, int32_t* ids, float* w, hipStream_t st) {
+  hipError_t err = hipSuccess;
   with_logits(a.bf16, [&](auto l) {
     typedef decltype(l) L;
     with_flag(a.sigmoid, [&](auto sig) {
       with_flag(bias != nullptr, [&](auto bi) {
         auto go = [&](auto kernel, int lanes) {
-          hipLaunchKernelGGL(kernel, route_grid(a.tokens, lanes), dim3(kRouteThreads), 0, st,
-                             (const typename L::elem*)a.logits, a.ld, bias, (int)a.tokens, (int)a.experts, (int)a.k,
-                             (int)a.renorm, a.scale, ids, w);
+          err = launch_in_parts(a.tokens, lanes, [&](int64_t t, int64_t n) {
+            hipLaunchKernelGGL(kernel, route_grid(n, lanes), dim3(kRouteThreads), 0, st,
+                               (const typename L::elem*)a.logits + t * a.ld, a.ld, bias, (int)n, (int)a.experts,
+                               (int)a.k, (int)a.renorm, a.scale, ids + t * a.k, w + t * a.k);
+          });
         };
         if (a.k <= kShort) {
           // A softmax uses its logits three times: held in registers, 177 tokens of
@@ -700,23 +703,27 @@ hipError_t launch_moe_route(const MoeRoute& a, const float* bias, int32_t* ids, 
       });
     });
   });
-  return hipGetLastError();
+  return err;
 }
 
 hipError_t launch_moe_route_bwd(const MoeRoute& a, const float* dw, const int32_t* ids, void* dl, int64_t ld_dl,
                                 hipStream_t st) {
+  hipError_t err = hipSuccess;
   with_logits(a.bf16, [&](auto l) {
     typedef decltype(l) L;
     typedef typename L::elem E;
     with_layout(a, [&](auto lanes, auto v) {
       with_flag(a.sigmoid, [&](auto sig) {
-        hipLaunchKernelGGL((k_route_bwd<L, lanes.value, v.value, sig.value>), route_grid(a.tokens, lanes.value),
-                           dim3(kRouteThreads), 0, st, dw, (const E*)a.logits, a.ld, ids, (int)a.tokens,
-                           (int)a.experts, (int)a.k, (int)a.renorm, a.scale, (E*)dl, ld_dl);
+        err = launch_in_parts(a.tokens, lanes.value, [&](int64_t t, int64_t n) {
+          hipLaunchKernelGGL((k_route_bwd<L, lanes.value, v.value, sig.value>), route_grid(n, lanes.value),
+                             dim3(kRouteThreads), 0, st, dw + t * a.k, (const E*)a.logits + t * a.ld, a.ld,
+                             ids + t * a.k, (int)n, (int)a.experts, (int)a.k, (int)a.renorm, a.scale,
+                             (E*)dl + t * ld_dl, ld_dl);
+        });
       });
     });
   });
-  return hipGetLastError();
+  return err;
 }
 
 }  // namespace fp8q

@@ -398,22 +398,25 @@ hipError_t launch_moe_combine_bwd(const MoeRows& a, const void* dy, int64_t ld_d
                                   const float* w, float* dw, hipStream_t st) {
   const Shape h = shape_of(a.cols);
   const int parts = (int)((a.k + kPair - 1) / kPair);
-  const uint32_t grid = (uint32_t)(h.wide ? a.tokens * parts : (a.tokens * parts + 15) / 16);
+  hipError_t err = hipSuccess;
   with_row(a.bf16, [&](auto row) {
     typedef decltype(row) Row;
     typedef typename Row::elem E;
     with_outputs(a, [&](auto fr, auto fc, auto past) {
       with_flag(h.wide, [&](auto wide) {
         with_flag(streamed(a), [&](auto nti) {
-          hipLaunchKernelGGL((k_combine_bwd<Row, fr.value, fc.value, wide.value, past.value, nti.value>), dim3(grid),
-                             dim3(h.threads), 0, st, (const E*)dy, ld_dy, (const E*)yp, ld_yp, a.dst, w,
-                             (int)a.tokens, (int)a.k, (int)(a.tokens * a.k), (E*)a.rows, a.ld_rows, a.q, a.ld_q,
-                             a.s, a.ld_s, dw, (int)a.cols, parts);
+          err = launch_in_parts(a.tokens, parts * (h.wide ? h.threads : 16), [&](int64_t t, int64_t n) {
+            const uint32_t grid = (uint32_t)(h.wide ? n * parts : (n * parts + 15) / 16);
+            hipLaunchKernelGGL((k_combine_bwd<Row, fr.value, fc.value, wide.value, past.value, nti.value>),
+                               dim3(grid), dim3(h.threads), 0, st, (const E*)dy + t * ld_dy, ld_dy, (const E*)yp,
+                               ld_yp, a.dst + t * a.k, w + t * a.k, (int)n, (int)a.k, (int)(a.tokens * a.k),
+                               (E*)a.rows, a.ld_rows, a.q, a.ld_q, a.s, a.ld_s, dw + t * a.k, (int)a.cols, parts);
+          });
         });
       });
     });
   });
-  return hipGetLastError();
+  return err;
 }
 
 }  // namespace fp8q
