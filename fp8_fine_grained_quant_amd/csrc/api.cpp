@@ -772,8 +772,9 @@ fp8q_status fp8q_moe_combine_bwd(const void* dy, const void* yp, fp8q_dtype t, i
 
 int64_t fp8q_grad_clip_workspace(int64_t n) {
   if (n < 0 || n > kMaxDim) return -1;
-  // per launch: partial sums, and the table the second pass reads
-  return cdiv(n, fp8q::kMaxClipTensors) * (fp8q::kClipBlocks * (int64_t)sizeof(double) + (int64_t)sizeof(fp8q::ClipBatch));
+  if (n == 0) return 0;
+  // partial sums, and for each launch the table the second pass reads
+  return fp8q::kClipBlocks * (int64_t)sizeof(double) + cdiv(n, fp8q::kMaxClipTensors) * (int64_t)sizeof(fp8q::ClipBatch);
 }
 
 fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, double max_norm, void* workspace,
@@ -794,8 +795,7 @@ fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, dou
   // tables of up to kMaxClipTensors non-empty tensors, one launch each and pass
   static_assert(sizeof(fp8q::ClipBatch) % 8 == 0, "tables follow each other");
   double* const part = static_cast<double*>(workspace);
-  fp8q::ClipBatch* const tables =
-      reinterpret_cast<fp8q::ClipBatch*>(part + cdiv(n, fp8q::kMaxClipTensors) * fp8q::kClipBlocks);
+  fp8q::ClipBatch* const tables = reinterpret_cast<fp8q::ClipBatch*>(part + fp8q::kClipBlocks);
   int parts = 0, batches = 0;
   fp8q::ClipBatch b;
   for (int64_t i = 0; i < n;) {
@@ -811,10 +811,7 @@ fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, dou
       ++b.n;
     }
     if (b.n == 0) break;
-    int blocks = 0;
-    if (fp8q::launch_grad_sumsq(b, tables + batches, part + parts, &blocks, stream) != hipSuccess)
-      return FP8Q_ERR_LAUNCH;
-    parts += blocks;
+    if (fp8q::launch_grad_sumsq(b, tables + batches, part, &parts, stream) != hipSuccess) return FP8Q_ERR_LAUNCH;
     ++batches;
   }
   // the second pass of the batches before the last: counted again from the sizes

@@ -81,7 +81,7 @@ __device__ __forceinline__ void load_chunk(const float* g, int len, float (&v)[k
 
 template <int N>
 __global__ __launch_bounds__(kClipThreads) void k_grad_sumsq(const ClipTable<N> b, ClipBatch* __restrict__ table,
-                                                             double* __restrict__ part) {
+                                                             double* __restrict__ part, int held) {
   __shared__ double red[4];
   const ClipFinder<N> find(b);
   if (blockIdx.x == gridDim.x - 1) {  // the second pass reads the table from memory
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kClipThreads) void k_grad_sumsq(const ClipTable<N> 
       for (int j = 0; j < 4; ++j) s = __builtin_fma((double)v[l][j], (double)v[l][j], s);
   }
   s = block_sum(s, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
+  if (threadIdx.x == 0) part[blockIdx.x] = (int)blockIdx.x < held ? part[blockIdx.x] + s : s;
 }
 
 template <bool OUT_BF16, int NT>
@@ -164,12 +164,15 @@ __global__ __launch_bounds__(kClipThreads) void k_grad_scale(const ClipBatch* __
   }
 }
 
-// Blocks of one launch: at most kClipBlocks, so that the partial sums every
-// scaling block adds up stay few.
+// Blocks of one launch: at most kClipBlocks.  A batch's blocks add to the
+// partial sums of the batches before it (launches of one stream follow each
+// other), so that all of them, which every scaling block adds up, stay that few
+// whatever the number of tensors (4000 of 100000 elements to BF16: 1077 us; 2230
+// with a batch's sums beside the others').
 int clip_blocks(int chunks) { return chunks < 1 ? 1 : chunks < kClipBlocks ? chunks : kClipBlocks; }
 
 template <int N>
-hipError_t sumsq(const ClipBatch& b, ClipBatch* table, double* part, int blocks, hipStream_t st) {
+hipError_t sumsq(const ClipBatch& b, ClipBatch* table, double* part, int held, int blocks, hipStream_t st) {
   ClipTable<N> t;
   t.n = b.n;
   for (int i = 0; i < b.n; ++i) {
@@ -179,7 +182,7 @@ hipError_t sumsq(const ClipBatch& b, ClipBatch* table, double* part, int blocks,
     t.last[i] = b.last[i];
   }
   t.cum[b.n] = b.cum[b.n];
-  hipLaunchKernelGGL(k_grad_sumsq<N>, dim3(blocks), dim3(kClipThreads), 0, st, t, table, part);
+  hipLaunchKernelGGL(k_grad_sumsq<N>, dim3(blocks), dim3(kClipThreads), 0, st, t, table, part, held);
   return hipGetLastError();
 }
 
@@ -187,12 +190,13 @@ hipError_t sumsq(const ClipBatch& b, ClipBatch* table, double* part, int blocks,
 
 // The table's size is that of a few classes: a launch with 2.7 KB of arguments
 // takes 4.4 us on the host, one without 3.0.
-hipError_t launch_grad_sumsq(const ClipBatch& b, ClipBatch* table, double* part, int* blocks, hipStream_t st) {
-  *blocks = clip_blocks(b.cum[b.n]);
-  if (b.n <= 8) return sumsq<8>(b, table, part, *blocks, st);
-  if (b.n <= 32) return sumsq<32>(b, table, part, *blocks, st);
-  if (b.n <= 64) return sumsq<64>(b, table, part, *blocks, st);
-  return sumsq<kMaxClipTensors>(b, table, part, *blocks, st);
+hipError_t launch_grad_sumsq(const ClipBatch& b, ClipBatch* table, double* part, int* held, hipStream_t st) {
+  const int blocks = clip_blocks(b.cum[b.n]), before = *held;
+  if (blocks > before) *held = blocks;
+  if (b.n <= 8) return sumsq<8>(b, table, part, before, blocks, st);
+  if (b.n <= 32) return sumsq<32>(b, table, part, before, blocks, st);
+  if (b.n <= 64) return sumsq<64>(b, table, part, before, blocks, st);
+  return sumsq<kMaxClipTensors>(b, table, part, before, blocks, st);
 }
 
 hipError_t launch_grad_scale(const ClipBatch* table, int chunks, bool out_bf16, const double* part, int parts,

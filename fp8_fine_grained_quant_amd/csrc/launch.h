@@ -180,7 +180,7 @@ hipError_t launch_moe_combine_bwd(const MoeRows& a, const void* dy, int64_t ld_d
 
 // ------------------------------------------------------- gradient clipping
 constexpr int kMaxClipTensors = 96;  // per launch: the table travels in the kernel's arguments
-constexpr int kClipBlocks = 2048;    // most blocks, and partial sums, per launch
+constexpr int kClipBlocks = 2048;    // most blocks of a launch, and partial sums of all of them
 constexpr int kClipChunk = 8192;     // elements of one tensor a block takes at a time
 // Up to N tensors, none of them empty.
 template <int N>
@@ -192,9 +192,10 @@ struct ClipTable {
   uint16_t n;
 };
 typedef ClipTable<kMaxClipTensors> ClipBatch;
-// The sums of squares of the batch's chunks, *blocks of them; leaves the table
-// in `table` (device memory) for the second pass.
-hipError_t launch_grad_sumsq(const ClipBatch& b, ClipBatch* table, double* part, int* blocks, hipStream_t st);
+// Adds the sums of squares of the batch's chunks to the *held partial sums, of
+// which there may then be more; leaves the table in `table` (device memory) for
+// the second pass.
+hipError_t launch_grad_sumsq(const ClipBatch& b, ClipBatch* table, double* part, int* held, hipStream_t st);
 hipError_t launch_grad_scale(const ClipBatch* table, int chunks, bool out_bf16, const double* part, int parts,
                              double max_norm, float* norm, hipStream_t st);
 
