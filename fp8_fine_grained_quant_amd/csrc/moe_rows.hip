@@ -279,7 +279,6 @@ __global__ __launch_bounds__(WIDE ? kWideThreads : 256) void k_combine_bwd(
       for (int i = 0; i < waves; ++i) sum += red[i][threadIdx.x];
       dw[p0 + j0 + threadIdx.x] = sum;
     }
-    __syncthreads();
   } else {
 #pragma unroll
     for (int u = 0; u < J; ++u)

@@ -77,7 +77,6 @@ struct RowBF16 {
     return (uint32_t)max(m[0], m[1]) << 16;
   }
   __device__ __forceinline__ static float load1(const elem* p) { return bf16_to_f32(*p); }
-  __device__ __forceinline__ static void store1(elem* p, float v) { *p = (elem)pack2_bf16(v, 0.f); }
 };
 
 struct RowF32 {
@@ -101,7 +100,6 @@ struct RowF32 {
     return m;
   }
   __device__ __forceinline__ static float load1(const elem* p) { return *p; }
-  __device__ __forceinline__ static void store1(elem* p, float v) { *p = v; }
 };
 
 // True if no lane of the wave has a run that column `end` cuts or that lies
