@@ -6,14 +6,16 @@
 // vanishes in the norm, and it does not depend on how the elements are spread
 // over threads beyond the last FP64 bits; the order of every sum is fixed.  The
 // factor and its products are in 64 bits as well (the times are the same with
-// FP32 products): the only rounding to fewer is the output's.  Two
-// passes over the data, since the factor needs the whole norm first; both are
-// bound by memory.  470M gradients (1.88 GB) to BF16: 773 us, 6.1 TB/s over the
-// 4.7 GB of both passes.  The second pass reads and writes past the caches
-// (20M gradients 43 us so, 55 us through them; the 470M 773 and 851), the first
-// does not, so that the second finds there what fits (20M: 49 us if it does).
-// Going backwards in the second pass, to meet the last gradients read first,
-// measured slower (798 us), as did 4 or 16 loads in flight (812, 797).
+// FP32 products): the only rounding to fewer is the output's.
+//
+// Two passes over the data, since the factor needs the whole norm first; both
+// are bound by memory.  470M gradients (1.88 GB) to BF16: 765 us, 6.1 TB/s over
+// the 4.7 GB of both passes (6.2 in the first, which only reads).  The second
+// pass reads and writes past the caches (20M gradients 43 us so, 55 us through
+// them; the 470M 773 and 851), the first does not, so that the second finds
+// there what fits (20M: 49 us where the first passes them too).  Going backwards
+// in the second pass, to meet the last gradients read first, measured slower
+// (798 us), as did 4 or 16 loads in flight (812, 797).
 
 #include "launch.h"
 #include "row_io.h"
@@ -31,7 +33,8 @@ constexpr int kClipStep = kClipThreads * 4;  // elements of one load of the whol
 static_assert(kClipStep * kClipLoads == kClipChunk, "a chunk is one round of loads");
 
 // Finds a chunk's tensor: a lane holds two of the tensors' first chunks, so
-// that the table is read once, not searched through its memory.
+// that the table is not searched through its memory; the tensor's own entries
+// are read from it.
 template <int N>
 struct ClipFinder {
   const ClipTable<N>& b;
@@ -188,8 +191,9 @@ hipError_t sumsq(const ClipBatch& b, ClipBatch* table, double* part, int held, i
 
 }  // namespace
 
-// The table's size is that of a few classes: a launch with 2.7 KB of arguments
-// takes 4.4 us on the host, one without 3.0.
+// The table's size is that of a few classes: a launch takes 2.9 us on the host
+// with 16 bytes of arguments, 3.4 with the table of 32 tensors (712 bytes), 3.7
+// with that of 64 (1416) and 3.9 with that of 96 (2120).
 hipError_t launch_grad_sumsq(const ClipBatch& b, ClipBatch* table, double* part, int* held, hipStream_t st) {
   const int blocks = clip_blocks(b.cum[b.n]), before = *held;
   if (blocks > before) *held = blocks;
