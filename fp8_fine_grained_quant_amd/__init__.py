@@ -28,6 +28,12 @@ tensors in place of pointer + leading dimension):
     fp8q_moe_combine(yp, dst, weights, y)
     fp8q_moe_combine_bwd(dy, yp, dst, weights, dweights, rows=None, q=None, scale=None)
     fp8q_grad_clip(grads, out, max_norm, norm, workspace)
+    fp8q_rms_norm(x, weight, eps, y, q, scale, rstd, residual=None, sum=None)     # a training block
+    fp8q_rms_norm_bwd(dy, x, weight, rstd, dweight, workspace, dx, q, scale, dsum=None)
+    fp8q_gemm_swiglu(xq, xs, wq, ws, h, gu=None, q=None, scale=None, workspace=None)
+    fp8q_grouped_gemm_swiglu(xq, xs, wq, ws, offsets, h, gu=None, q=None, scale=None)
+    fp8q_gemm_dgrad_swiglu(dyq, dys, wq_t, ws, gu, dgu, h=None)
+    fp8q_grouped_gemm_dgrad_swiglu(dyq, dys, wq_t, ws, offsets, gu, dgu, h=None)
 
 Each GEMM also takes exact=True, which calls the *_exact entry point (BF16
 matrix instruction on exactly converted codes: the exact-accumulation variant).
@@ -37,9 +43,12 @@ quant_weight_128x128, quant_transpose, gemm_fprop, gemm_dgrad, gemm_wgrad,
 grouped_gemm, quant_mx, quant_mx_transpose, gemm_mx, grouped_gemm_mx, grouped_gemm_mx_dgrad (and those of the MoE
 backward and the dual-output quantizer); moe_route, moe_route_bwd, moe_sort,
 moe_dispatch, moe_dispatch_quant, moe_dispatch_bwd, moe_combine,
-moe_combine_bwd, moe_combine_bwd_quant, grad_clip.
+moe_combine_bwd, moe_combine_bwd_quant, grad_clip; rms_norm, rms_norm_quant,
+rms_norm_bwd, rms_norm_bwd_quant, gemm_swiglu, gemm_swiglu_quant,
+grouped_gemm_swiglu, grouped_gemm_swiglu_quant, gemm_dgrad_swiglu,
+grouped_gemm_dgrad_swiglu, adamw (with adamw_states).
 
-The MoE routing and clipping calls take tensors of the current device (a
+The MoE routing, clipping and training block's calls take tensors of the current device (a
 stream object given to a call that allocates makes its device the current one)
 and refuse others.
 """
@@ -68,7 +77,10 @@ EXPORTS = ["fp8q_status_string", "fp8q_set_gemm_tile", "fp8q_quant_act_1x128", "
            "fp8q_grouped_gemm_mx_dgrad", "fp8q_gemm_fprop_quant", "fp8q_gemm_dgrad_quant",
            "fp8q_gemm_fprop_interval", "fp8q_quant_batch", "fp8q_moe_route", "fp8q_moe_route_bwd",
            "fp8q_moe_sort", "fp8q_moe_sort_workspace", "fp8q_moe_dispatch", "fp8q_moe_dispatch_bwd",
-           "fp8q_moe_combine", "fp8q_moe_combine_bwd", "fp8q_grad_clip", "fp8q_grad_clip_workspace"]
+           "fp8q_moe_combine", "fp8q_moe_combine_bwd", "fp8q_grad_clip", "fp8q_grad_clip_workspace",
+           "fp8q_rms_norm", "fp8q_rms_norm_bwd", "fp8q_rms_norm_bwd_workspace", "fp8q_gemm_swiglu",
+           "fp8q_gemm_swiglu_workspace", "fp8q_grouped_gemm_swiglu", "fp8q_gemm_dgrad_swiglu",
+           "fp8q_grouped_gemm_dgrad_swiglu", "fp8q_adamw"]
 
 
 MAX_QUANT_JOBS = 8
@@ -118,7 +130,8 @@ def _open(path):
     if not os.path.exists(path):
         raise RuntimeError(f"{os.path.basename(path)} not built ({path}); run __graft_entry__.build()")
     lib = ctypes.CDLL(path)
-    P, I64, I32, F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    P, I64, I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    F32, F64 = ctypes.c_float, ctypes.c_double
     sig = {
         "fp8q_status_string": ([I32], ctypes.c_char_p),
         "fp8q_set_gemm_tile": ([I32], I32),
@@ -152,6 +165,16 @@ def _open(path):
         "fp8q_moe_combine_bwd": ([P, P, I32, I64, I64, I64, I64, P, I32, P, P, I64, P, I64, P, I64, P, P], I32),
         "fp8q_grad_clip": ([P, I64, I32, ctypes.c_double, P, I64, P, P], I32),
         "fp8q_grad_clip_workspace": ([I64], I64),
+        "fp8q_rms_norm": ([P, I32, I64, I64, I64, P, I64, P, F32, P, I64, P, I64, P, I64, P, I64, P, P], I32),
+        "fp8q_rms_norm_bwd": ([P, P, I32, I64, I64, I64, I64, P, P, P, I64, P, I64, P, I64, P, I64, P, P, I64, P],
+                              I32),
+        "fp8q_rms_norm_bwd_workspace": ([I64, I64], I64),
+        "fp8q_gemm_swiglu": ([P, P, P, P, I64, I64, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P], I32),
+        "fp8q_gemm_swiglu_workspace": ([I64, I64, I32], I64),
+        "fp8q_grouped_gemm_swiglu": ([P, P, P, P, P, I64, I64, I64, I64, P, I64, P, I64, P, I64, P, I64, P], I32),
+        "fp8q_gemm_dgrad_swiglu": ([P, P, P, P, I64, I64, I64, P, I64, P, I64, P, I64, P], I32),
+        "fp8q_grouped_gemm_dgrad_swiglu": ([P, P, P, P, P, I64, I64, I64, I64, P, I64, P, I64, P, I64, P], I32),
+        "fp8q_adamw": ([P, I64, I32, I32, F64, F64, F64, F64, F64, I64, ctypes.c_uint64, P, F64, P], I32),
     }
     for name in ["fp8q_gemm_fprop", "fp8q_gemm_dgrad", "fp8q_gemm_wgrad", "fp8q_grouped_gemm"]:
         sig[name + "_exact"] = sig[name]
@@ -792,6 +815,8 @@ def _bind(lib):
     names = [n for n in EXPORTS if n.startswith(("fp8q_moe_", "fp8q_grad_"))]
     _calls.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, _current_device,
                 _current_stream, _check, _score, _on_stream)
+    names = [n for n in EXPORTS if "rms_norm" in n or "swiglu" in n or "adamw" in n]
+    _calls.bind_block({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names})
     return _calls
 
 
@@ -942,3 +967,168 @@ def grad_clip(grads, max_norm, out=None, stream=None):
     tensors of their shapes; None: in place).  Returns the norm before
     clipping, a 0-dim tensor on the GPU."""
     return _native().grad_clip(grads, out, max_norm, None, None, stream)
+
+
+# ------------------------------------------------------------- training block
+_GATE_UP = 4
+
+
+def fp8q_rms_norm(x, weight, eps, y, q, scale, rstd, residual=None, sum=None, stream=None):
+    """RMS norm of x (+ residual, the sum then left in `sum`): y of x's type
+    and / or the codes and scales of it, rstd [rows] FP32."""
+    _required(rstd=rstd)
+    _native().rms_norm(x, weight, residual, eps, y, q, scale, sum, rstd, None, stream)
+
+
+def rms_norm_bwd_workspace(rows, cols):
+    """Bytes of workspace that fp8q_rms_norm_bwd needs on the current device."""
+    n = load_library().fp8q_rms_norm_bwd_workspace(rows, cols)
+    if n < 0:
+        raise ValueError(f"{rows} rows of {cols}: out of range (at most {MAX_NORM_COLS} columns)")
+    return n
+
+
+def fp8q_rms_norm_bwd(dy, x, weight, rstd, dweight, workspace, dx=None, q=None, scale=None, dsum=None, stream=None):
+    """Gradient of the norm of x: dx (+ dsum, the stream's own) and / or its
+    codes and scales, dweight [cols] FP32.  workspace:
+    rms_norm_bwd_workspace(rows, cols) bytes (uint8)."""
+    _required(dweight=dweight)
+    _native().rms_norm_bwd(dy, x, weight, rstd, dsum, dx, q, scale, dweight, workspace, None, stream)
+
+
+def gemm_swiglu_workspace(rows, width, codes):
+    """Bytes of workspace that fp8q_gemm_swiglu needs (codes: q is wanted)."""
+    return load_library().fp8q_gemm_swiglu_workspace(rows, width, int(bool(codes)))
+
+
+def fp8q_gemm_swiglu(xq, xs, wq, ws, h, gu=None, q=None, scale=None, workspace=None, stream=None):
+    """Gated feed-forward block: h [M, N] BF16 (or None) = silu(x Wg^T) (x Wu^T)
+    for wq [2N, K], gate rows before up rows; gu [M, 2N] BF16 keeps both
+    products, q and scale are h's codes.  workspace: gemm_swiglu_workspace(M, N,
+    q is not None) bytes (uint8), None if 0."""
+    _native().gemm_swiglu(xq, xs, wq, ws, None, h, gu, q, scale, workspace, None, stream)
+
+
+def fp8q_grouped_gemm_swiglu(xq, xs, wq, ws, offsets, h, gu=None, q=None, scale=None, stream=None):
+    """The same by expert: wq [E, 2N, K], device offsets [E + 1]."""
+    _required(offsets=offsets)
+    _native().gemm_swiglu(xq, xs, wq, ws, offsets, h, gu, q, scale, None, None, stream)
+
+
+def fp8q_gemm_dgrad_swiglu(dyq, dys, wq_t, ws, gu, dgu, h=None, stream=None):
+    """Gradient of gate and up, dgu [M, 2K] BF16 (may be gu itself), through the
+    output projection's Dgrad (operands of fp8q_gemm_dgrad); h [M, K] BF16: the
+    block's output again."""
+    _required(dgu=dgu)
+    _native().gemm_dgrad_swiglu(dyq, dys, wq_t, ws, None, gu, dgu, h, False, stream)
+
+
+def fp8q_grouped_gemm_dgrad_swiglu(dyq, dys, wq_t, ws, offsets, gu, dgu, h=None, stream=None):
+    """The same by expert (operands of fp8q_grouped_gemm_dgrad)."""
+    _required(offsets=offsets, dgu=dgu)
+    _native().gemm_dgrad_swiglu(dyq, dys, wq_t, ws, offsets, gu, dgu, h, False, stream)
+
+
+MAX_NORM_COLS = 16384
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, stream=None):
+    """Root-mean-square norm of the rows of x, or of x + residual: (y, sum,
+    rstd).  sum is the stream that goes on (None without a residual), rstd
+    [rows] FP32 is for the gradient.  Rows and codes made here start on 64-byte
+    segments, as those of moe_dispatch."""
+    y, _, _, total, rstd = _native().rms_norm(x, weight, residual, eps, None, None, None, None, None, _ROWS, stream)
+    return y, total, rstd
+
+
+def rms_norm_quant(x, weight, residual=None, eps=1e-6, with_output=False, stream=None):
+    """The norm with its 1x128 quantization, of y before its rounding to x's
+    type: (y or None, q, scale, sum, rstd)."""
+    want = _ROWS | _CODES if with_output else _CODES
+    return _native().rms_norm(x, weight, residual, eps, None, None, None, None, None, want, stream)
+
+
+def rms_norm_bwd(dy, x, weight, rstd, dsum=None, stream=None):
+    """Gradient of rms_norm: (dx, dweight).  x: what was normalized (the sum
+    where there was a residual); dsum: the gradient of the stream that went on,
+    which joins dx."""
+    out = _native().rms_norm_bwd(dy, x, weight, rstd, dsum, None, None, None, None, None, _ROWS, stream)
+    return out[0], out[3]
+
+
+def rms_norm_bwd_quant(dy, x, weight, rstd, dsum=None, with_output=True, stream=None):
+    """Gradient of the norm with dx also (or only) as 1x128 codes, of dx before
+    its rounding: (dx or None, q, scale, dweight)."""
+    want = _ROWS | _CODES if with_output else _CODES
+    return _native().rms_norm_bwd(dy, x, weight, rstd, dsum, None, None, None, None, None, want, stream)
+
+
+def gemm_swiglu(xq, xs, wq, ws, with_gu=False, stream=None):
+    """Gated feed-forward block: (h BF16 [M, N], gu BF16 [M, 2N] or None) of
+    codes xq [M, K] and stacked weight codes wq [2N, K], gate before up."""
+    want = _ROWS | (_GATE_UP if with_gu else 0)
+    return _native().gemm_swiglu(xq, xs, wq, ws, None, None, None, None, None, None, want, stream)[:2]
+
+
+def gemm_swiglu_quant(xq, xs, wq, ws, with_output=False, with_gu=False, stream=None):
+    """The block with the 1x128 quantization of h, before its rounding to BF16:
+    (h or None, gu or None, q, scale)."""
+    want = _CODES | (_ROWS if with_output else 0) | (_GATE_UP if with_gu else 0)
+    return _native().gemm_swiglu(xq, xs, wq, ws, None, None, None, None, None, None, want, stream)
+
+
+def grouped_gemm_swiglu(xq, xs, wq, ws, offsets, with_gu=False, stream=None):
+    """gemm_swiglu by expert: wq [E, 2N, K], rows [o_e, o_{e+1}) of xq."""
+    _required(offsets=offsets)
+    want = _ROWS | (_GATE_UP if with_gu else 0)
+    return _native().gemm_swiglu(xq, xs, wq, ws, offsets, None, None, None, None, None, want, stream)[:2]
+
+
+def grouped_gemm_swiglu_quant(xq, xs, wq, ws, offsets, with_output=False, with_gu=False, stream=None):
+    """gemm_swiglu_quant by expert."""
+    _required(offsets=offsets)
+    want = _CODES | (_ROWS if with_output else 0) | (_GATE_UP if with_gu else 0)
+    return _native().gemm_swiglu(xq, xs, wq, ws, offsets, None, None, None, None, None, want, stream)
+
+
+def gemm_dgrad_swiglu(dyq, dys, wq_t, ws, gu, with_h=False, stream=None):
+    """Gradient of gate and up through the output projection's Dgrad, and with
+    with_h the block's output again: (dgu BF16 [M, 2K], h BF16 [M, K] or None)."""
+    return _native().gemm_dgrad_swiglu(dyq, dys, wq_t, ws, None, gu, None, None, with_h, stream)
+
+
+def grouped_gemm_dgrad_swiglu(dyq, dys, wq_t, ws, offsets, gu, with_h=False, stream=None):
+    """gemm_dgrad_swiglu by expert (operands of grouped_gemm_dgrad)."""
+    _required(offsets=offsets)
+    return _native().gemm_dgrad_swiglu(dyq, dys, wq_t, ws, offsets, gu, None, None, with_h, stream)
+
+
+def adamw_states(params, bits=32):
+    """New states of adamw's exp_avg, exp_avg_sq and scales for `params`:
+    FP32 zeros and None, or (bits=8) codes and their scales."""
+    if bits not in (8, 32):
+        raise ValueError(f"bits: {bits!r}, expected 8 or 32")
+    def new(dtype):
+        return [torch.zeros(p.shape, dtype=dtype, device=p.device) for p in params]
+
+    def scales():
+        return [torch.zeros(_cdiv(p.numel(), 128), dtype=torch.float32, device=p.device) for p in params]
+
+    if bits == 32:
+        return new(torch.float32), new(torch.float32), None
+    return new(torch.uint8), new(torch.uint8), (scales(), scales())
+
+
+def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0, scales=None,
+          seed=0, norm=None, max_norm=float("inf"), copies=None, stream=None):
+    """One AdamW step (number `step`, from 1 on) of FP32 params, in place.
+    grads: FP32 or BF16.  exp_avg, exp_avg_sq: FP32, or with scales (two lists
+    of FP32 [ceil(n / 128)]) the E4M3 codes of the first moment and of the
+    second one's root, rounded at random by `seed` (another one for every
+    step).  norm: the gradients' norm (0-dim FP32 on the GPU, from grad_clip with
+    max_norm=inf), by which the step clips them to max_norm.  copies: BF16
+    tensors that receive the new parameters."""
+    m_scales, v_scales = scales if scales is not None else (None, None)
+    beta1, beta2 = betas
+    _native().adamw(params, grads, exp_avg, exp_avg_sq, m_scales, v_scales, copies, lr, beta1, beta2, eps, weight_decay,
+                    step, seed, norm, max_norm, stream)

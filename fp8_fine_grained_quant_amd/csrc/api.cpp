@@ -8,12 +8,14 @@
 #include "../../include/fp8q.h"
 #include "launch.h"
 
-#include <atomic>
 #include <stdint.h>
-#ifdef FP8Q_DEBUG
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
 #include <new>
+#include <utility>
 #include <vector>
-#endif
 
 namespace fp8q {
 
@@ -826,6 +828,315 @@ fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, dou
     if (fp8q::launch_grad_scale(tables + k, chunk_count, ot == FP8Q_BF16, part, parts, max_norm,
                                 k == 0 ? norm : nullptr, stream) != hipSuccess)
       return FP8Q_ERR_LAUNCH;
+  }
+  return FP8Q_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------- gated feed-forward block
+namespace {
+
+// A launch's threads are counted in 32 bits: tiles of 512 threads, and the
+// few-row kernel's workgroups of 512 threads and 8 columns.
+constexpr int64_t kMaxTiles = ((int64_t(1) << 32) - 1) / 512;
+constexpr int64_t kMaxFewWidth = 8 * kMaxTiles;
+bool few_rows(int64_t M, int64_t N) { return M <= fp8q::kFewRows && N <= kMaxFewWidth; }
+
+// The sizes of the gated block's entry points: outputs of gate and of up each,
+// contraction length, 256-row tiles.
+fp8q_status check_gated(int64_t M, int64_t width, int64_t inner, int64_t tiles_m) {
+  if (M < 0 || width < 0 || inner < 0 || M > kMaxDim || width > kMaxDim / 2 || inner > kMaxDim) return FP8Q_ERR_SHAPE;
+  if (width % 128 != 0 || inner % 128 != 0 || inner > kMaxContraction) return FP8Q_ERR_SHAPE;
+  if (M == 0 || width == 0) return FP8Q_OK;
+  if (inner == 0) return FP8Q_ERR_SHAPE;  // an empty contraction would leave the outputs undefined
+  return tiles_m * (width / 128) > kMaxTiles ? FP8Q_ERR_SHAPE : FP8Q_OK;
+}
+
+// BF16 matrices of the gated block's entry points, NULL where they are not given.
+fp8q_status check_bf16(const void* p, int64_t ld, int64_t cols) {
+  return p ? check_gemm_out(p, FP8Q_BF16, ld, cols) : FP8Q_OK;
+}
+
+fp8q_status check_swiglu_out(const void* h, int64_t ld_h, const void* gu, int64_t ld_gu, const uint8_t* q, int64_t ld_q,
+                             const float* s, int64_t ld_s, int64_t N) {
+  if (!h && !gu && !q) return FP8Q_ERR_NULL;
+  if (const fp8q_status c = check_bf16(h, ld_h, N); c != FP8Q_OK) return c;
+  if (const fp8q_status c = check_bf16(gu, ld_gu, 2 * N); c != FP8Q_OK) return c;
+  return q || s ? check_quant_out(q, ld_q, s, ld_s, N) : FP8Q_OK;
+}
+
+GemmArgs swiglu_args(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t M, int64_t N,
+                     int64_t K, void* h, int64_t ld_h, void* gu, int64_t ld_gu, uint8_t* q, int64_t ld_q, float* s,
+                     int64_t ld_s) {
+  GemmArgs a{};
+  a.A = xq; a.B = wq; a.sa = xs; a.sb = ws; a.C = h;
+  a.lda = K; a.ldb = K; a.ld_sa = K / 128; a.sb_rs = K / 128; a.sb_cs = 1; a.ldc = ld_h;
+  a.M = M; a.N = N; a.K = K;
+  a.sb_mode = fp8q::kSbBlock; a.gated = fp8q::kSwiglu;
+  a.gu = static_cast<uint16_t*>(gu); a.ld_gu = ld_gu;
+  a.qo = q; a.ld_qo = ld_q; a.so = s; a.ld_so = ld_s;
+  return a;
+}
+
+// The gradient's matrices: gu and dgu [rows, 2K], h optional [rows, K].
+fp8q_status check_dswiglu(const void* gu, int64_t ld_gu, const void* dgu, int64_t ld_dgu, const void* h, int64_t ld_h,
+                          int64_t K) {
+  if (!gu || !dgu) return FP8Q_ERR_NULL;
+  if (const fp8q_status c = check_bf16(gu, ld_gu, 2 * K); c != FP8Q_OK) return c;
+  if (const fp8q_status c = check_bf16(dgu, ld_dgu, 2 * K); c != FP8Q_OK) return c;
+  return check_bf16(h, ld_h, K);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t fp8q_gemm_swiglu_workspace(int64_t M, int64_t N, int codes) {
+  if (M < 0 || N < 0 || M > kMaxDim || N > kMaxDim / 2) return -1;
+  return codes && few_rows(M, N) ? M * N * (int64_t)sizeof(float) : 0;
+}
+
+fp8q_status fp8q_gemm_swiglu(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t M,
+                             int64_t N, int64_t K, void* h, int64_t ld_h, void* gu, int64_t ld_gu, uint8_t* q,
+                             int64_t ld_q, float* scale, int64_t ld_s, void* workspace, int64_t workspace_bytes,
+                             hipStream_t stream) {
+  if (const fp8q_status c = check_gated(M, N, K, cdiv(M, 256)); c != FP8Q_OK || M == 0 || N == 0) return c;
+  if (!xq || !xs || !wq || !ws) return FP8Q_ERR_NULL;
+  if (const fp8q_status c = check_swiglu_out(h, ld_h, gu, ld_gu, q, ld_q, scale, ld_s, N); c != FP8Q_OK) return c;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned4(xs) || !aligned4(ws)) return FP8Q_ERR_ALIGN;
+  const GemmArgs a = swiglu_args(xq, xs, wq, ws, M, N, K, h, ld_h, gu, ld_gu, q, ld_q, scale, ld_s);
+  if (few_rows(M, N)) {
+    const int64_t need = fp8q_gemm_swiglu_workspace(M, N, q != nullptr);
+    if (need > 0) {
+      if (!workspace) return FP8Q_ERR_NULL;
+      if (!aligned16(workspace)) return FP8Q_ERR_ALIGN;
+      if (workspace_bytes < need) return FP8Q_ERR_SHAPE;
+    }
+    return launched(fp8q::launch_swiglu_few(a, q ? static_cast<float*>(workspace) : nullptr, stream));
+  }
+  return launched(fp8q::launch_gemm(a, stream));
+}
+
+fp8q_status fp8q_grouped_gemm_swiglu(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                                     const int32_t* offsets, int64_t E, int64_t M_total, int64_t N, int64_t K, void* h,
+                                     int64_t ld_h, void* gu, int64_t ld_gu, uint8_t* q, int64_t ld_q, float* scale,
+                                     int64_t ld_s, hipStream_t stream) {
+  if (E < 1 || E > 65536) return FP8Q_ERR_SHAPE;
+  if (const fp8q_status c = check_gated(M_total, N, K, cdiv(M_total, 256) + E); c != FP8Q_OK || M_total == 0 || N == 0)
+    return c;
+  if (!xq || !xs || !wq || !ws || !offsets) return FP8Q_ERR_NULL;
+  if (const fp8q_status c = check_swiglu_out(h, ld_h, gu, ld_gu, q, ld_q, scale, ld_s, N); c != FP8Q_OK) return c;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned4(xs) || !aligned4(ws) || !aligned4(offsets)) return FP8Q_ERR_ALIGN;
+  if (const fp8q_status d = debug_check_offsets(offsets, E, M_total, stream); d != FP8Q_OK) return d;
+  GemmArgs a = swiglu_args(xq, xs, wq, ws, M_total, N, K, h, ld_h, gu, ld_gu, q, ld_q, scale, ld_s);
+  a.offsets = offsets; a.E = E; a.b_estride = 2 * N * K; a.sb_estride = (2 * N / 128) * (K / 128);
+  return launched(fp8q::launch_gemm(a, stream));
+}
+
+fp8q_status fp8q_gemm_dgrad_swiglu(const uint8_t* dyq, const float* dys, const uint8_t* wq_t, const float* ws,
+                                   int64_t M, int64_t N, int64_t K, const void* gu, int64_t ld_gu, void* dgu,
+                                   int64_t ld_dgu, void* h, int64_t ld_h, hipStream_t stream) {
+  if (const fp8q_status c = check_gated(M, K, N, cdiv(M, 256)); c != FP8Q_OK || M == 0 || K == 0) return c;
+  if (!dyq || !dys || !wq_t || !ws) return FP8Q_ERR_NULL;
+  if (const fp8q_status c = check_dswiglu(gu, ld_gu, dgu, ld_dgu, h, ld_h, K); c != FP8Q_OK) return c;
+  if (!aligned16(dyq) || !aligned16(wq_t) || !aligned4(dys) || !aligned4(ws)) return FP8Q_ERR_ALIGN;
+  GemmArgs a{};  // the product of fp8q_gemm_dgrad
+  a.A = dyq; a.B = wq_t; a.sa = dys; a.sb = ws; a.C = dgu;
+  a.lda = N; a.ldb = N; a.ld_sa = N / 128; a.sb_rs = 1; a.sb_cs = K / 128; a.ldc = ld_dgu;
+  a.M = M; a.N = K; a.K = N;
+  a.sb_mode = fp8q::kSbBlock; a.gated = fp8q::kDSwiglu;
+  a.gu = static_cast<uint16_t*>(const_cast<void*>(gu)); a.ld_gu = ld_gu;
+  a.h = static_cast<uint16_t*>(h); a.ld_h = ld_h;
+  return launched(fp8q::launch_gemm(a, stream));
+}
+
+fp8q_status fp8q_grouped_gemm_dgrad_swiglu(const uint8_t* dyq, const float* dys, const uint8_t* wq_t, const float* ws,
+                                           const int32_t* offsets, int64_t E, int64_t M_total, int64_t N, int64_t K,
+                                           const void* gu, int64_t ld_gu, void* dgu, int64_t ld_dgu, void* h,
+                                           int64_t ld_h, hipStream_t stream) {
+  if (E < 1 || E > 65536) return FP8Q_ERR_SHAPE;
+  if (N > 0 && E * N > INT32_MAX / 256) return FP8Q_ERR_SHAPE;  // as fp8q_grouped_gemm_dgrad
+  if (const fp8q_status c = check_gated(M_total, K, N, cdiv(M_total, 256) + E); c != FP8Q_OK || M_total == 0 || K == 0)
+    return c;
+  if (!dyq || !dys || !wq_t || !ws || !offsets) return FP8Q_ERR_NULL;
+  if (const fp8q_status c = check_dswiglu(gu, ld_gu, dgu, ld_dgu, h, ld_h, K); c != FP8Q_OK) return c;
+  if (!aligned16(dyq) || !aligned16(wq_t) || !aligned4(dys) || !aligned4(ws) || !aligned4(offsets))
+    return FP8Q_ERR_ALIGN;
+  if (const fp8q_status d = debug_check_offsets(offsets, E, M_total, stream); d != FP8Q_OK) return d;
+  GemmArgs a{};  // the product of fp8q_grouped_gemm_dgrad
+  a.A = dyq; a.B = wq_t; a.sa = dys; a.sb = ws; a.C = dgu;
+  a.lda = N; a.ldb = E * N; a.ld_sa = N / 128; a.sb_rs = 1; a.sb_cs = K / 128; a.ldc = ld_dgu;
+  a.M = M_total; a.N = K; a.K = N;
+  a.sb_mode = fp8q::kSbBlock; a.gated = fp8q::kDSwiglu;
+  a.offsets = offsets; a.E = E; a.b_estride = N; a.sb_estride = (N / 128) * (K / 128);
+  a.gu = static_cast<uint16_t*>(const_cast<void*>(gu)); a.ld_gu = ld_gu;
+  a.h = static_cast<uint16_t*>(h); a.ld_h = ld_h;
+  return launched(fp8q::launch_gemm(a, stream));
+}
+
+}  // extern "C"
+
+// --------------------------------------------------------------- RMS norm
+namespace {
+
+fp8q_status check_norm(fp8q_dtype t, int64_t rows, int64_t cols) {
+  if (!valid_dtype(t)) return FP8Q_ERR_DTYPE;
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > fp8q::kMaxNormCols) return FP8Q_ERR_SHAPE;
+  return FP8Q_OK;
+}
+
+// The output rows and / or codes of the norm's entry points.
+fp8q_status check_norm_out(const void* out, fp8q_dtype t, int64_t ld, const uint8_t* q, int64_t ld_q, const float* s,
+                           int64_t ld_s, int64_t cols) {
+  if (!out && !q) return FP8Q_ERR_NULL;
+  if (out)
+    if (const fp8q_status c = check_rows(out, t, ld, cols); c != FP8Q_OK) return c;
+  return q || s ? check_codes(q, ld_q, s, ld_s, cols) : FP8Q_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8q_status fp8q_rms_norm(const void* x, fp8q_dtype t, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                          int64_t ld_r, const float* weight, float eps, void* y, int64_t ld_y, uint8_t* q, int64_t ld_q,
+                          float* scale, int64_t ld_s, void* sum, int64_t ld_sum, float* rstd, hipStream_t stream) {
+  if (const fp8q_status c = check_norm(t, rows, cols); c != FP8Q_OK) return c;
+  if (!(eps >= 0.f) || eps - eps != 0.f) return FP8Q_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return FP8Q_OK;
+  if (const fp8q_status c = check_rows(x, t, ld_x, cols); c != FP8Q_OK) return c;
+  if (residual) {
+    if (const fp8q_status c = check_rows(residual, t, ld_r, cols); c != FP8Q_OK) return c;
+    if (const fp8q_status c = check_rows(sum, t, ld_sum, cols); c != FP8Q_OK) return c;
+  }
+  if (!weight || !rstd) return FP8Q_ERR_NULL;
+  if (const fp8q_status c = check_norm_out(y, t, ld_y, q, ld_q, scale, ld_s, cols); c != FP8Q_OK) return c;
+  if (!aligned4(weight) || !aligned4(rstd)) return FP8Q_ERR_ALIGN;
+  const fp8q::NormRows a{t == FP8Q_BF16, rows, cols, weight, y, ld_y, q, ld_q, scale, ld_s};
+  return launched(fp8q::launch_rms_norm(a, x, ld_x, residual, ld_r, eps, sum, ld_sum, rstd, stream));
+}
+
+int64_t fp8q_rms_norm_bwd_workspace(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > fp8q::kMaxNormCols) return -1;
+  return rows == 0 || cols == 0 ? 0 : fp8q::rms_norm_parts(rows, cols) * cols * (int64_t)sizeof(float);
+}
+
+fp8q_status fp8q_rms_norm_bwd(const void* dy, const void* x, fp8q_dtype t, int64_t rows, int64_t cols, int64_t ld_dy,
+                              int64_t ld_x, const float* weight, const float* rstd, const void* dsum, int64_t ld_dsum,
+                              void* dx, int64_t ld_dx, uint8_t* q, int64_t ld_q, float* scale, int64_t ld_s,
+                              float* dweight, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (const fp8q_status c = check_norm(t, rows, cols); c != FP8Q_OK || cols == 0) return c;
+  if (!dweight) return FP8Q_ERR_NULL;
+  if (!aligned4(dweight)) return FP8Q_ERR_ALIGN;
+  if (rows > 0) {
+    if (const fp8q_status c = check_rows(dy, t, ld_dy, cols); c != FP8Q_OK) return c;
+    if (const fp8q_status c = check_rows(x, t, ld_x, cols); c != FP8Q_OK) return c;
+    if (dsum)
+      if (const fp8q_status c = check_rows(dsum, t, ld_dsum, cols); c != FP8Q_OK) return c;
+    if (!weight || !rstd || !workspace) return FP8Q_ERR_NULL;
+    if (const fp8q_status c = check_norm_out(dx, t, ld_dx, q, ld_q, scale, ld_s, cols); c != FP8Q_OK) return c;
+    if (!aligned4(weight) || !aligned4(rstd) || !aligned4(workspace)) return FP8Q_ERR_ALIGN;
+    if (workspace_bytes < fp8q_rms_norm_bwd_workspace(rows, cols)) return FP8Q_ERR_SHAPE;
+  }
+  const fp8q::NormRows a{t == FP8Q_BF16, rows, cols, weight, dx, ld_dx, q, ld_q, scale, ld_s};
+  return launched(fp8q::launch_rms_norm_bwd(a, dy, ld_dy, x, ld_x, rstd, dsum, ld_dsum, static_cast<float*>(workspace),
+                                            dweight, stream));
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ AdamW
+namespace {
+
+uint32_t mix32(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x6C8E9CF5u;
+  x = (x ^ (x >> 15)) * 0xB2D05E13u;
+  return x ^ (x >> 16);
+}
+
+// Whether two of the tensors' parameters share memory (a tensor given twice).
+bool params_overlap(const fp8q_adamw_tensor* t, int64_t n) {
+  // ordered as they are as a rule given: one pass; else every pair's order by a sort on the side
+  bool rising = true, falling = true;
+  const float *end = nullptr, *begin = nullptr;
+  for (int64_t i = 0; i < n; ++i) {
+    if (t[i].len == 0) continue;
+    if (end) {
+      rising = rising && t[i].p >= end;
+      falling = falling && t[i].p + t[i].len <= begin;
+    }
+    end = t[i].p + t[i].len;
+    begin = t[i].p;
+  }
+  if (rising || falling) return false;
+  std::vector<std::pair<const float*, int64_t>> at;
+  at.reserve((size_t)n);
+  for (int64_t i = 0; i < n; ++i)
+    if (t[i].len > 0) at.emplace_back(t[i].p, t[i].len);
+  std::sort(at.begin(), at.end());
+  for (size_t i = 1; i < at.size(); ++i)
+    if (at[i].first < at[i - 1].first + at[i - 1].second) return true;
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int64_t n, fp8q_dtype gt, int bits, double lr, double beta1,
+                       double beta2, double eps, double weight_decay, int64_t step, uint64_t seed, const float* norm,
+                       double max_norm, hipStream_t stream) {
+  if (!valid_dtype(gt)) return FP8Q_ERR_DTYPE;
+  if (n < 0 || n > kMaxDim || (bits != 8 && bits != 32) || step < 1) return FP8Q_ERR_SHAPE;
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || !(max_norm >= 0.0) ||
+      lr - lr != 0.0 || eps - eps != 0.0 || weight_decay - weight_decay != 0.0)
+    return FP8Q_ERR_SHAPE;
+  if (n == 0) return FP8Q_OK;
+  if (!tensors) return FP8Q_ERR_NULL;
+  if (!aligned4(norm)) return FP8Q_ERR_ALIGN;
+  int64_t chunks = 0;  // of all tensors: counted in 32 bits
+  for (int64_t i = 0; i < n; ++i) {
+    const fp8q_adamw_tensor& t = tensors[i];
+    if (t.len < 0 || (chunks += cdiv(t.len, fp8q::kAdamChunk)) > kMaxDim / 2) return FP8Q_ERR_SHAPE;
+    if (t.len == 0) continue;
+    if (!t.p || !t.g || !t.m || !t.v || (bits == 8 && (!t.m_scale || !t.v_scale))) return FP8Q_ERR_NULL;
+    if (!aligned4(t.p) || !aligned_to(t.g, esize(gt)) || !aligned_to(t.copy, 2)) return FP8Q_ERR_ALIGN;
+    if (bits == 32 ? !aligned4(t.m) || !aligned4(t.v) : !aligned4(t.m_scale) || !aligned4(t.v_scale))
+      return FP8Q_ERR_ALIGN;
+  }
+  try {
+    if (params_overlap(tensors, n)) return FP8Q_ERR_SHAPE;
+  } catch (const std::bad_alloc&) {  // no memory for the check
+    return FP8Q_ERR_LAUNCH;
+  }
+  fp8q::AdamStep a;
+  a.beta1 = (float)beta1; a.rest1 = (float)(1.0 - beta1);
+  a.beta2 = (float)beta2; a.rest2 = (float)(1.0 - beta2);
+  a.keep = (float)(1.0 - lr * weight_decay);
+  a.step = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
+  a.root = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+  a.eps = (float)eps;
+  a.norm = norm;
+  a.max_norm = max_norm;
+  const uint32_t lo = (uint32_t)seed, hi = (uint32_t)(seed >> 32);
+  fp8q::AdamBatch b;
+  for (int64_t i = 0; i < n;) {
+    b.n = 0;
+    b.cum[0] = 0;
+    for (; i < n && b.n < fp8q::kMaxAdamTensors; ++i) {
+      const fp8q_adamw_tensor& t = tensors[i];
+      const int64_t c = cdiv(t.len, fp8q::kAdamChunk);
+      if (c == 0) continue;
+      const int k = b.n++;
+      b.p[k] = t.p; b.g[k] = t.g; b.m[k] = t.m; b.v[k] = t.v;
+      b.m_scale[k] = t.m_scale; b.v_scale[k] = t.v_scale; b.copy[k] = t.copy;
+      b.last[k] = (uint16_t)(t.len - (c - 1) * fp8q::kAdamChunk);
+      b.cum[k + 1] = b.cum[k] + (int)c;
+      b.key[k] = mix32(mix32(lo + 0x9E3779B1u * (uint32_t)i) + hi);
+    }
+    if (b.n == 0) break;
+    if (fp8q::launch_adamw(b, a, gt == FP8Q_BF16, bits == 8, stream) != hipSuccess) return FP8Q_ERR_LAUNCH;
   }
   return FP8Q_OK;
 }

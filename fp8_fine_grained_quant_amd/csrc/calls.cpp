@@ -1,5 +1,5 @@
-// The Python calls of the MoE routing operators and of gradient clipping: what
-// stands between a call and the library's entry point (argument checks,
+// The Python calls of the MoE routing operators, of gradient clipping and of the
+// training block's operators (norm, gated block, AdamW): what stands between a call and the library's entry point (argument checks,
 // allocation of outputs, the current stream) in native code.  Their kernels on
 // a decode step take 2 us, a launch 3 us; with that part in Python a call took
 // 13 to 16 us (57 us for the clipping of 60 tensors), and so took every call
@@ -46,6 +46,17 @@ struct Library {
   decltype(&fp8q_grad_clip) grad_clip;
   decltype(&fp8q_grad_clip_workspace) grad_clip_workspace;
 } lib;
+struct BlockLibrary {
+  decltype(&fp8q_rms_norm) rms_norm;
+  decltype(&fp8q_rms_norm_bwd) rms_norm_bwd;
+  decltype(&fp8q_rms_norm_bwd_workspace) rms_norm_bwd_workspace;
+  decltype(&fp8q_gemm_swiglu) gemm_swiglu;
+  decltype(&fp8q_gemm_swiglu_workspace) gemm_swiglu_workspace;
+  decltype(&fp8q_grouped_gemm_swiglu) grouped_gemm_swiglu;
+  decltype(&fp8q_gemm_dgrad_swiglu) gemm_dgrad_swiglu;
+  decltype(&fp8q_grouped_gemm_dgrad_swiglu) grouped_gemm_dgrad_swiglu;
+  decltype(&fp8q_adamw) adamw;
+} block;
 PyObject *current_device, *current_stream, *raise_status, *score_code, *on_stream;  // Python callables
 
 // ------------------------------------------------------------------ arguments
@@ -606,16 +617,345 @@ PyObject* grad_clip(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------- the training block's calls
+void contiguous(std::initializer_list<const Tensor*> ts) {
+  for (const Tensor* t : ts)
+    if (t && !t->is_contiguous())
+      refuse(PyExc_ValueError, "operands, scales, weights, statistics and workspaces must be contiguous");
+}
+constexpr int kWantRows = 1, kWantCodes = 2, kWantGateUp = 4;
+
+// x, weight, residual, eps, y, q, scale, sum, rstd, want, stream; with want None
+// the outputs are given (sum where there is a residual)
+PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 11);
+  if (a[9] != Py_None && a[n - 1] != Py_None) return again_on("rms_norm", a, n);
+  const Tensor &x = tensor(a[0], "x"), &weight = tensor(a[1], "weight");
+  const Tensor *residual = optional(a[2], "residual"), *sum = optional(a[7], "sum"), *rstd = optional(a[8], "rstd");
+  const float eps = (float)real(a[3]);
+  RowOutputs out(a[4], a[5], a[6]);
+  matrix(x, "x");
+  const int64_t rows = x.size(0), cols = x.size(1);
+  expect(&weight, {cols}, at::kFloat, "weight");
+  if (residual) expect(residual, {rows, cols}, x.scalar_type(), "residual");
+  const bool make_outputs = a[9] != Py_None;
+  if (!make_outputs) {
+    if (residual) expect(sum, {rows, cols}, x.scalar_type(), "sum");
+    expect(rstd, {rows}, at::kFloat, "rstd");
+  }
+  out.expect_all(rows, cols, x.scalar_type());
+  const c10::Device device = on_gpu({&x, &weight, residual, sum, rstd, out.rows, out.q, out.scale});
+  contiguous({&weight, rstd});
+  const fp8q_dtype type = type_of(x);
+  Tensor own_sum, own_rstd;
+  if (make_outputs) {
+    out.allocate(small(a[9]), rows, cols, x);
+    if (residual) {
+      own_sum = RowOutputs::spaced(rows, cols, (int64_t)x.element_size(), x.scalar_type(), x);
+      sum = &own_sum;
+    }
+    rstd = &given_or(nullptr, own_rstd, {rows}, at::kFloat, x);
+  }
+  const int64_t ld = stride(x), ld_r = residual ? stride(*residual) : 0, ld_s = residual ? stride(*sum) : 0,
+                ld_y = out.ld_rows(), ld_q = out.ld_q(), ld_sc = out.ld_scale();
+  const hipStream_t st = stream_of(a[10], device);
+  check(unlocked([&] {
+          return block.rms_norm(data<void>(x), type, rows, cols, ld, data<void>(residual), ld_r, data<float>(weight),
+                                eps, data<void>(out.rows), ld_y, data<uint8_t>(out.q), ld_q, data<float>(out.scale),
+                                ld_sc, residual ? data<void>(sum) : nullptr, ld_s, data<float>(rstd), st);
+        }),
+        "fp8q_rms_norm");
+  if (!make_outputs) return none();
+  return pack({wrap_or_none(out.own_rows), wrap_or_none(out.own_q), wrap_or_none(out.own_scale),
+               wrap_or_none(own_sum), THPVariable_Wrap(own_rstd)});
+  END_HANDLE_TH_ERRORS
+}
+
+// dy, x, weight, rstd, dsum, dx, q, scale, dweight, workspace, want, stream; with
+// want None the outputs and the workspace are given
+PyObject* rms_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 12);
+  if (a[10] != Py_None && a[n - 1] != Py_None) return again_on("rms_norm_bwd", a, n);
+  const Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x"), &weight = tensor(a[2], "weight"),
+               &rstd = tensor(a[3], "rstd");
+  const Tensor *dsum = optional(a[4], "dsum"), *dweight = optional(a[8], "dweight"), *ws = optional(a[9], "workspace");
+  RowOutputs out(a[5], a[6], a[7]);
+  matrix(dy, "dy");
+  const int64_t rows = dy.size(0), cols = dy.size(1);
+  expect(&x, {rows, cols}, dy.scalar_type(), "x");
+  expect(&weight, {cols}, at::kFloat, "weight");
+  expect(&rstd, {rows}, at::kFloat, "rstd");
+  if (dsum) expect(dsum, {rows, cols}, dy.scalar_type(), "dsum");
+  const bool make_outputs = a[10] != Py_None;
+  if (!make_outputs) {
+    expect(dweight, {cols}, at::kFloat, "dweight");
+    if (ws) expect(ws, {-1}, at::kByte, "workspace");
+  }
+  out.expect_all(rows, cols, dy.scalar_type());
+  const c10::Device device = on_gpu({&dy, &x, &weight, &rstd, dsum, dweight, ws, out.rows, out.q, out.scale});
+  contiguous({&weight, &rstd, dweight, ws});
+  const fp8q_dtype type = type_of(dy);
+  Tensor own_dw, own_ws;
+  const hipStream_t st = stream_of(a[11], device);
+  if (make_outputs) {
+    out.allocate(small(a[10]), rows, cols, dy);
+    dweight = &given_or(nullptr, own_dw, {cols}, at::kFloat, dy);
+    const int64_t need = block.rms_norm_bwd_workspace(rows, cols);
+    if (need < 0) check(FP8Q_ERR_SHAPE, "fp8q_rms_norm_bwd");
+    if (need) ws = &given_or(nullptr, own_ws, {need}, at::kByte, dy);
+  }
+  const int64_t ld_dy = stride(dy), ld_x = stride(x), ld_s = dsum ? stride(*dsum) : 0, ld_dx = out.ld_rows(),
+                ld_q = out.ld_q(), ld_sc = out.ld_scale();
+  check(unlocked([&] {
+          return block.rms_norm_bwd(data<void>(dy), data<void>(x), type, rows, cols, ld_dy, ld_x, data<float>(weight),
+                                    data<float>(rstd), data<void>(dsum), ld_s, data<void>(out.rows), ld_dx,
+                                    data<uint8_t>(out.q), ld_q, data<float>(out.scale), ld_sc, data<float>(dweight),
+                                    data<void>(ws), ws ? ws->numel() : 0, st);
+        }),
+        "fp8q_rms_norm_bwd");
+  if (!make_outputs) return none();
+  return pack({wrap_or_none(out.own_rows), wrap_or_none(out.own_q), wrap_or_none(out.own_scale),
+               THPVariable_Wrap(own_dw)});
+  END_HANDLE_TH_ERRORS
+}
+
+int64_t groups(int64_t n) { return (n + 127) / 128; }
+
+// xq, xs, wq, ws, offsets, h, gu, q, scale, workspace, want, stream; offsets None:
+// dense; with want None the outputs and the workspace are given
+PyObject* gemm_swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 12);
+  if (a[10] != Py_None && a[n - 1] != Py_None) return again_on("gemm_swiglu", a, n);
+  const Tensor &xq = tensor(a[0], "xq"), &xs = tensor(a[1], "xs"), &wq = tensor(a[2], "wq"), &ws = tensor(a[3], "ws");
+  const Tensor *offsets = optional(a[4], "offsets"), *gu = optional(a[6], "gu"), *room = optional(a[9], "workspace");
+  const Tensor *h = optional(a[5], "h"), *q = optional(a[7], "q"), *scale = optional(a[8], "scale");
+  matrix(xq, "xq");
+  const int64_t m = xq.size(0), k = xq.size(1);
+  if (wq.dim() != (offsets ? 3 : 2))
+    refuse(PyExc_ValueError, "wq: shape " + text_of(wq.sizes()) + ", expected " +
+                                 (offsets ? "[experts, 2 * width, K]" : "[2 * width, K]"));
+  const int64_t both = wq.size(-2), width = both / 2, experts = offsets ? wq.size(0) : 1;
+  if (both % 2) refuse(PyExc_ValueError, "wq: " + std::to_string(both) + " rows, expected as many of up as of gate");
+  expect(&xq, {m, k}, at::kByte, "xq");
+  expect(&xs, {m, groups(k)}, at::kFloat, "xs");
+  if (offsets) {
+    expect(&wq, {experts, both, k}, at::kByte, "wq");
+    expect(&ws, {experts, groups(both), groups(k)}, at::kFloat, "ws");
+    expect(offsets, {experts + 1}, at::kInt, "offsets");
+  } else {
+    expect(&wq, {both, k}, at::kByte, "wq");
+    expect(&ws, {groups(both), groups(k)}, at::kFloat, "ws");
+  }
+  if (h) expect(h, {m, width}, at::kBFloat16, "h");
+  if (gu) expect(gu, {m, both}, at::kBFloat16, "gu");
+  if (q || scale) {
+    expect(q, {m, width}, at::kByte, "q");
+    expect(scale, {m, groups(width)}, at::kFloat, "scale");
+  }
+  if (room) expect(room, {-1}, at::kByte, "workspace");
+  const c10::Device device = on_gpu({&xq, &xs, &wq, &ws, offsets, h, gu, q, scale, room});
+  contiguous({&xq, &xs, &wq, &ws, offsets, room});
+  const bool make_outputs = a[10] != Py_None;
+  Tensor own_h, own_gu, own_q, own_scale, own_room;
+  const hipStream_t st = stream_of(a[11], device);
+  if (make_outputs) {
+    const int want = small(a[10]);
+    if (want & kWantRows) h = &given_or(nullptr, own_h, {m, width}, at::kBFloat16, xq);
+    if (want & kWantGateUp) gu = &given_or(nullptr, own_gu, {m, both}, at::kBFloat16, xq);
+    if (want & kWantCodes) {
+      q = &given_or(nullptr, own_q, {m, width}, at::kByte, xq);
+      scale = &given_or(nullptr, own_scale, {m, groups(width)}, at::kFloat, xq);
+    }
+    const int64_t need = offsets ? 0 : block.gemm_swiglu_workspace(m, width, q != nullptr);
+    if (need < 0) check(FP8Q_ERR_SHAPE, "fp8q_gemm_swiglu");
+    if (need) room = &given_or(nullptr, own_room, {need}, at::kByte, xq);
+  }
+  const int64_t ld_h = h ? stride(*h) : 0, ld_gu = gu ? stride(*gu) : 0, ld_q = q ? stride(*q) : 0,
+                ld_s = scale ? stride(*scale) : 0;
+  check(unlocked([&] {
+          if (offsets)
+            return block.grouped_gemm_swiglu(data<uint8_t>(xq), data<float>(xs), data<uint8_t>(wq), data<float>(ws),
+                                             data<int32_t>(offsets), experts, m, width, k, data<void>(h), ld_h,
+                                             data<void>(gu), ld_gu, data<uint8_t>(q), ld_q, data<float>(scale), ld_s,
+                                             st);
+          return block.gemm_swiglu(data<uint8_t>(xq), data<float>(xs), data<uint8_t>(wq), data<float>(ws), m, width, k,
+                                   data<void>(h), ld_h, data<void>(gu), ld_gu, data<uint8_t>(q), ld_q,
+                                   data<float>(scale), ld_s, data<void>(room), room ? room->numel() : 0, st);
+        }),
+        offsets ? "fp8q_grouped_gemm_swiglu" : "fp8q_gemm_swiglu");
+  if (!make_outputs) return none();
+  return pack({wrap_or_none(own_h), wrap_or_none(own_gu), wrap_or_none(own_q), wrap_or_none(own_scale)});
+  END_HANDLE_TH_ERRORS
+}
+
+// dyq, dys, wq_t, ws, offsets, gu, dgu, h, with_h, stream; offsets None: dense;
+// with dgu None it, and h if with_h, are allocated
+PyObject* gemm_dgrad_swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 10);
+  if (a[6] == Py_None && a[n - 1] != Py_None) return again_on("gemm_dgrad_swiglu", a, n);
+  const Tensor &dyq = tensor(a[0], "dyq"), &dys = tensor(a[1], "dys"), &wq_t = tensor(a[2], "wq_t"),
+               &ws = tensor(a[3], "ws"), &gu = tensor(a[5], "gu");
+  const Tensor *offsets = optional(a[4], "offsets"), *dgu = optional(a[6], "dgu"), *h = optional(a[7], "h");
+  matrix(dyq, "dyq");
+  matrix(wq_t, "wq_t");
+  const int64_t m = dyq.size(0), inner = dyq.size(1), width = wq_t.size(0);
+  if (offsets && (offsets->dim() != 1 || offsets->size(0) < 2))
+    refuse(PyExc_ValueError, "offsets: shape " + text_of(offsets->sizes()) + ", expected [experts + 1]");
+  const int64_t experts = offsets ? offsets->size(0) - 1 : 1;
+  expect(&dyq, {m, inner}, at::kByte, "dyq");
+  expect(&dys, {m, groups(inner)}, at::kFloat, "dys");
+  expect(&wq_t, {width, experts * inner}, at::kByte, "wq_t");
+  expect(&ws, {groups(experts * inner), groups(width)}, at::kFloat, "ws");
+  if (offsets) expect(offsets, {experts + 1}, at::kInt, "offsets");
+  expect(&gu, {m, 2 * width}, at::kBFloat16, "gu");
+  if (dgu) expect(dgu, {m, 2 * width}, at::kBFloat16, "dgu");
+  if (h) expect(h, {m, width}, at::kBFloat16, "h");
+  const c10::Device device = on_gpu({&dyq, &dys, &wq_t, &ws, offsets, &gu, dgu, h});
+  contiguous({&dyq, &dys, &wq_t, &ws, offsets});
+  Tensor own_dgu, own_h;
+  const hipStream_t st = stream_of(a[9], device);
+  const bool make_outputs = dgu == nullptr;
+  if (make_outputs) {
+    dgu = &given_or(nullptr, own_dgu, {m, 2 * width}, at::kBFloat16, dyq);
+    if (truth(a[8])) h = &given_or(nullptr, own_h, {m, width}, at::kBFloat16, dyq);
+  }
+  const int64_t ld_gu = stride(gu), ld_d = stride(*dgu), ld_h = h ? stride(*h) : 0;
+  check(unlocked([&] {
+          if (offsets)
+            return block.grouped_gemm_dgrad_swiglu(data<uint8_t>(dyq), data<float>(dys), data<uint8_t>(wq_t),
+                                                   data<float>(ws), data<int32_t>(offsets), experts, m, inner, width,
+                                                   data<void>(gu), ld_gu, data<void>(dgu), ld_d, data<void>(h), ld_h,
+                                                   st);
+          return block.gemm_dgrad_swiglu(data<uint8_t>(dyq), data<float>(dys), data<uint8_t>(wq_t), data<float>(ws), m,
+                                         inner, width, data<void>(gu), ld_gu, data<void>(dgu), ld_d, data<void>(h),
+                                         ld_h, st);
+        }),
+        offsets ? "fp8q_grouped_gemm_dgrad_swiglu" : "fp8q_gemm_dgrad_swiglu");
+  if (!make_outputs) return none();
+  return pack({THPVariable_Wrap(own_dgu), wrap_or_none(own_h)});
+  END_HANDLE_TH_ERRORS
+}
+
+// A tuple of the caller's list, which other code may change before the launch.
+THPObjectPtr fixed_list(PyObject* o, const char* what) {
+  THPObjectPtr items(PySequence_Fast(o, (std::string(what) + ": expected a sequence of tensors").c_str()));
+  THPObjectPtr t(items ? PySequence_Tuple(items.get()) : nullptr);
+  if (!t) throw python_error();
+  return t;
+}
+
+// params, grads, exp_avg, exp_avg_sq, m_scales, v_scales, copies, lr, beta1, beta2,
+// eps, weight_decay, step, seed, norm, max_norm, stream; scales None: states in 32 bits
+PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 17);
+  enum { kP, kG, kM, kV, kMs, kVs, kCopy, kLists };
+  static const char* const names[kLists] = {"params",     "grads",      "exp_avg", "exp_avg_sq",
+                                            "exp_avg scales", "exp_avg_sq scales", "copies"};
+  THPObjectPtr lists[kLists];
+  Py_ssize_t tensors = 0;
+  if ((a[kMs] == Py_None) != (a[kVs] == Py_None)) refuse(PyExc_ValueError, "scales of one state and not of the other");
+  for (int l = 0; l < kLists; ++l) {
+    if (l >= kMs && a[l] == Py_None) continue;
+    lists[l] = fixed_list(a[l], names[l]);
+    const Py_ssize_t len = PyTuple_GET_SIZE(lists[l].get());
+    if (l == 0) tensors = len;
+    if (len != tensors)
+      refuse(PyExc_ValueError, std::string(names[l]) + ": " + std::to_string(len) + " tensors for " +
+                                   std::to_string(tensors) + " parameters");
+  }
+  const double lr = real(a[7]), beta1 = real(a[8]), beta2 = real(a[9]), eps = real(a[10]), decay = real(a[11]);
+  const int64_t step = integer(a[12]);
+  const uint64_t seed = PyLong_AsUnsignedLongLong(a[13]);
+  if (PyErr_Occurred()) throw python_error();
+  const Tensor* norm = optional(a[14], "norm");
+  const double max_norm = real(a[15]);
+  const bool codes = lists[kMs].get() != nullptr;
+  const ScalarType state = codes ? at::kByte : at::kFloat;
+  ScalarType grad = at::kFloat;
+  c10::Device device(c10::kCUDA);
+  bool gpu = true;
+  const Tensor* abroad = nullptr;
+  std::vector<fp8q_adamw_tensor> table((size_t)tensors);
+  for (Py_ssize_t i = 0; i < tensors; ++i) {
+    const Tensor* t[kLists] = {};
+    for (int l = 0; l < kLists; ++l)
+      if (lists[l].get()) t[l] = &tensor(PyTuple_GET_ITEM(lists[l].get(), i), names[l]);
+    if (i == 0) {
+      grad = t[kG]->scalar_type();
+      device = t[kP]->device();
+    }
+    const ScalarType types[kLists] = {at::kFloat, grad, state, state, at::kFloat, at::kFloat, at::kBFloat16};
+    const int64_t scales = (t[kP]->numel() + 127) / 128;
+    for (int l = 0; l < kLists; ++l) {
+      if (!t[l]) continue;
+      if (l == kMs || l == kVs) expect(t[l], {scales}, types[l], names[l]);
+      else expect(t[l], t[kP]->sizes(), types[l], names[l]);
+      if (!t[l]->is_contiguous()) refuse(PyExc_ValueError, std::string(names[l]) + " must be contiguous");
+      gpu = gpu && t[l]->is_cuda();
+      if (t[l]->device() != device) abroad = t[l];
+    }
+  }
+  if (norm) {
+    expect(norm, {}, at::kFloat, "norm");
+    gpu = gpu && norm->is_cuda();
+    if (tensors == 0) device = norm->device();
+    if (norm->device() != device) abroad = norm;
+  }
+  if (!gpu) refuse_place();
+  if (abroad) refuse_devices(device, abroad->device());
+  if (grad != at::kFloat && grad != at::kBFloat16) refuse(PyExc_TypeError, "unsupported dtype " + name_of(grad));
+  const hipStream_t st = stream_of(a[16], device);
+  for (Py_ssize_t i = 0; i < tensors; ++i) {
+    auto at = [&](int l) -> const Tensor* {
+      return lists[l].get() ? &THPVariable_Unpack(PyTuple_GET_ITEM(lists[l].get(), i)) : nullptr;
+    };
+    table[(size_t)i] = {data<float>(at(kP)), data<void>(at(kG)), data<void>(at(kM)),      data<void>(at(kV)),
+                        data<float>(at(kMs)), data<float>(at(kVs)), data<uint16_t>(at(kCopy)), at(kP)->numel()};
+  }
+  check(unlocked([&] {
+          return block.adamw(table.data(), tensors, grad == at::kBFloat16 ? FP8Q_BF16 : FP8Q_F32, codes ? 8 : 32, lr,
+                             beta1, beta2, eps, decay, step, seed, data<float>(norm), max_norm, st);
+        }),
+        "fp8q_adamw");
+  return none();
+  END_HANDLE_TH_ERRORS
+}
+
+template <class F>
+void find_address(PyObject* addresses, F& f, const char* name) {
+  PyObject* o = PyDict_GetItemString(addresses, name);
+  void* p = o ? PyLong_AsVoidPtr(o) : nullptr;
+  if (!p) refuse(PyExc_ValueError, std::string("no address of ") + name);
+  f = reinterpret_cast<F>(p);
+}
+
+// {name: address} of the training block's entry points
+PyObject* bind_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  count(n, 1);
+  find_address(a[0], block.rms_norm, "fp8q_rms_norm");
+  find_address(a[0], block.rms_norm_bwd, "fp8q_rms_norm_bwd");
+  find_address(a[0], block.rms_norm_bwd_workspace, "fp8q_rms_norm_bwd_workspace");
+  find_address(a[0], block.gemm_swiglu, "fp8q_gemm_swiglu");
+  find_address(a[0], block.gemm_swiglu_workspace, "fp8q_gemm_swiglu_workspace");
+  find_address(a[0], block.grouped_gemm_swiglu, "fp8q_grouped_gemm_swiglu");
+  find_address(a[0], block.gemm_dgrad_swiglu, "fp8q_gemm_dgrad_swiglu");
+  find_address(a[0], block.grouped_gemm_dgrad_swiglu, "fp8q_grouped_gemm_dgrad_swiglu");
+  find_address(a[0], block.adamw, "fp8q_adamw");
+  return none();
+  END_HANDLE_TH_ERRORS
+}
+
 // {name: address}, current_device, current_stream, raise_status, score_code, on_stream
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   count(n, 6);
-  auto find = [&](auto& f, const char* name) {
-    PyObject* o = PyDict_GetItemString(a[0], name);
-    void* p = o ? PyLong_AsVoidPtr(o) : nullptr;
-    if (!p) refuse(PyExc_ValueError, std::string("no address of ") + name);
-    f = reinterpret_cast<std::decay_t<decltype(f)>>(p);
-  };
+  auto find = [&](auto& f, const char* name) { find_address(a[0], f, name); };
   find(lib.moe_route, "fp8q_moe_route");
   find(lib.moe_route_bwd, "fp8q_moe_route_bwd");
   find(lib.moe_sort, "fp8q_moe_sort");
@@ -639,7 +979,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind),         FAST(moe_route),    FAST(moe_route_bwd),   FAST(moe_sort),
                          FAST(moe_dispatch), FAST(moe_dispatch_bwd), FAST(moe_combine), FAST(moe_combine_bwd),
-                         FAST(grad_clip),    {nullptr, nullptr, 0, nullptr}};
+                         FAST(grad_clip),    FAST(bind_block),   FAST(rms_norm),        FAST(rms_norm_bwd),
+                         FAST(gemm_swiglu),  FAST(gemm_dgrad_swiglu), FAST(adamw),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

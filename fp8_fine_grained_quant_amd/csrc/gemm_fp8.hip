@@ -127,6 +127,14 @@ __device__ __forceinline__ void to_bf16_quarters(const v8i& f, v8bf (&out)[4]) {
   }
 }
 
+// What a kernel's epilogue does with the product.
+enum Epilogue : int {
+  kEpiStore = 0,    // store it
+  kEpiQuant = 1,    // its 1x128 codes as well (store_tile_q)
+  kEpiDSwiglu = 2,  // take it for a gated block's dh (store_tile_dswiglu)
+  kEpiSwiglu = 3    // gate and up of a gated block (wide tile only; store_tile_swiglu)
+};
+
 template <int V>
 struct IC {
   static constexpr int value = V;
@@ -143,7 +151,7 @@ __device__ __forceinline__ void row_scales(float v, float k, float (&out)[4]) {
 
 }  // namespace
 
-template <int SB_MODE, int OUT_F32, bool GROUPED, bool KG, bool SC4, bool EX, bool QO, int INTV>
+template <int SB_MODE, int OUT_F32, bool GROUPED, bool KG, bool SC4, bool EX, int EPI, int INTV>
 __global__ __launch_bounds__(kNT) void k_gemm_fp8(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass only needs the launch stub
   typedef Stage<SB_MODE, SC4> S;
@@ -521,9 +529,12 @@ __global__ __launch_bounds__(kNT) void k_gemm_fp8(GemmArgs p) {
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   __builtin_amdgcn_s_barrier();
   fence();
-  if constexpr (QO) {
+  if constexpr (EPI == kEpiQuant) {
     static_assert(!OUT_F32 && !KG && TR, "fused output quantization: BF16 Fprop/Dgrad only");
     store_tile_q<kTM, kTN, 32>(acc, st0 + w * 12288, po, tc.m0 + w * 64, tc.mend, tc.n0, lane);
+  } else if constexpr (EPI == kEpiDSwiglu) {
+    static_assert(!OUT_F32 && !KG && TR, "gated block's gradient: BF16 Dgrad only");
+    store_tile_dswiglu<kTM, kTN>(acc, st0 + w * 12288, po, tc.m0 + w * 64, tc.mend, tc.n0, lane);
   } else {
     store_tile<kTM, kTN, OUT_F32, OUT_F32 ? 16 : 32, 0, TR>(acc, st0 + w * 12288, po, tc.m0 + w * 64, tc.mend, tc.n0,
                                                             lane);
@@ -562,7 +573,14 @@ static_assert(kWIB == kTM, "one B load per slot of the last column");
 static_assert(kWDmaA <= kWDmaSlots && kWFirstSlot + kWDmaSlots <= kTM * (kTN - 1), "A loads between the barriers");
 static_assert(4 * kBM * kBK + 4 * 2 * kMaxChunks + 4 * 2 * 256 * 4 + 1024 <= 160 * 1024, "LDS of one CU");
 
-template <int OUT_F32, bool GROUPED, bool QO>
+//
+// EPI == kEpiSwiglu (a gated block's gate and up): the tile's 256 B rows are
+// 128 gate rows and the 128 up rows of the same outputs, N after them, and a
+// wave's strip holds both of its 64 output columns (sub-tiles 0-3 gate, 4-7
+// up), so the activation and the product are formed in registers.  SC4 false
+// (scale rows that are not 16-byte aligned): the row scales come 4 bytes per row
+// and chunk, into a ring of 8 chunks.
+template <int OUT_F32, bool GROUPED, int EPI, bool SC4 = true>
 __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   __shared__ __attribute__((aligned(16))) uint8_t sa0[kBM * kBK];
@@ -573,11 +591,12 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) float scA[2 * 256 * 4];         // row scales, 2 blocks of 4 chunks
   __shared__ __attribute__((aligned(16))) uint8_t dmy[1024];              // target of count-keeping loads
 
+  constexpr bool GLU = EPI == kEpiSwiglu;
   TileCoord tc;
-  if (!tile_coord<kBM, kWBN, GROUPED>(p, tc)) return;
+  if (!tile_coord<kBM, GLU ? kWBN / 2 : kWBN, GROUPED>(p, tc)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wr = w & 3, wc = w >> 2;  // the wave's 64-row strip and 128-column half
+  const int wr = w & 3, wc = w >> 2;  // the wave's 64-row strip and 128-column half (GLU: 64 outputs)
   const int l16 = lane & 15, g = lane >> 4;
   const int nk = (int)(p.K / kBK);
   const uint8_t* Bp = p.B + (GROUPED ? (int64_t)tc.e * p.b_estride : 0);
@@ -586,11 +605,13 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
 
   // direct-load sources, range-checked as in k_gemm_fp8
   const __amdgpu_buffer_rsrc_t rA = make_rsrc(p.A + tc.m0 * p.lda, (uint32_t)(rows * p.lda));
-  const __amdgpu_buffer_rsrc_t rB = make_rsrc(Bp + (int64_t)tc.n0 * p.ldb, (uint32_t)(kWBN * p.ldb));
+  // (GLU: waves 0-3 load the gate rows, waves 4-7 the up rows)
+  const int64_t b0 = tc.n0 + (GLU && wc ? p.N : 0);
+  const __amdgpu_buffer_rsrc_t rB = make_rsrc(Bp + b0 * p.ldb, (uint32_t)((GLU ? kWBN / 2 : kWBN) * p.ldb));
   const __amdgpu_buffer_rsrc_t rSa = make_rsrc(p.sa + tc.m0 * p.ld_sa, (uint32_t)(rows * p.ld_sa * 4));
   const int r8 = lane >> 3, lc = (lane & 7) ^ r8;
   const uint32_t voffA = (uint32_t)((w * kWIA * 8 + r8) * p.lda + 16 * lc);
-  const uint32_t voffB = (uint32_t)((w * kWIB * 8 + r8) * p.ldb + 16 * lc);
+  const uint32_t voffB = (uint32_t)(((GLU ? wr : w) * kWIB * 8 + r8) * p.ldb + 16 * lc);
   const uint32_t stepA = (uint32_t)(8 * p.lda), stepB = (uint32_t)(8 * p.ldb);
   const uint32_t voffSa = (uint32_t)(min(wr * 64 + lane, rows - 1) * p.ld_sa * 4);
 
@@ -602,10 +623,15 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_ptr)(ar + (w * kWIA + d) * 1024), 16, voffA + d * stepA,
                                                (uint32_t)kb * kBK, 0, 0);
     } else {
-      const bool real = w < 4 && (kb & 3) == 0;
-      uint8_t* dst = real ? reinterpret_cast<uint8_t*>(scA) + ((kb >> 2) & 1) * 4096 + w * 1024 : dmy;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rSa, (lds_ptr)dst, 16, real ? voffSa : kNoAccess, real ? (uint32_t)kb * 4 : 0u,
-                                               0, 0);
+      const bool real = w < 4 && (!SC4 || (kb & 3) == 0);
+      uint8_t* const ring = reinterpret_cast<uint8_t*>(scA);
+      uint8_t* dst = real ? ring + (SC4 ? ((kb >> 2) & 1) * 4096 + w * 1024 : (kb & 7) * 1024 + w * 256) : dmy;
+      if constexpr (SC4)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rSa, (lds_ptr)dst, 16, real ? voffSa : kNoAccess,
+                                                 real ? (uint32_t)kb * 4 : 0u, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rSa, (lds_ptr)dst, 4, real ? voffSa : kNoAccess,
+                                                 real ? (uint32_t)kb * 4 : 0u, 0, 0);
     }
   };
   auto issue_b = [&](int kb, uint8_t* br, int q) {
@@ -622,7 +648,7 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
     return make_frag(*reinterpret_cast<const uint4*>(base + offLo), *reinterpret_cast<const uint4*>(base + offHi));
   };
   auto rdB = [&](const uint8_t* br, int j) -> v8i {
-    const uint8_t* base = br + (wc * 128 + 16 * j) * kBK;
+    const uint8_t* base = br + (GLU ? (j >> 2) * 128 + wc * 64 + 16 * (j & 3) : wc * 128 + 16 * j) * kBK;
     return make_frag(*reinterpret_cast<const uint4*>(base + offLo), *reinterpret_cast<const uint4*>(base + offHi));
   };
   // B is the matrix instruction's first operand (as in k_gemm_fp8's block
@@ -632,7 +658,8 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
   auto rdSa = [&](int kb, float (&v)[kTM]) {
 #pragma unroll
     for (int i = 0; i < kTM; ++i) {
-      int off = ((kb >> 2) & 1) * 1024 + (wr * 64 + 16 * i + l16) * 4 + (kb & 3);
+      const int row = wr * 64 + 16 * i + l16;
+      int off = SC4 ? ((kb >> 2) & 1) * 1024 + row * 4 + (kb & 3) : (kb & 7) * 256 + row;
       asm volatile("" : "+v"(off));
       v[i] = scA[off];
     }
@@ -649,14 +676,24 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
   v8i a[kTM];          // A fragments of the current chunk
   v8i bring[2];        // B fragments: this column's and the next one's
   v4f pp[kTM];         // MFMA partials, ring indexed by slot % 4
-  float sc[kTM];       // row scales times the block's B scale
+  float sc[kTM];       // row scales times the block's B scale (GLU: the gate's)
+  float scu[kTM];      // GLU: the up block's
   float sa_nx[kTM] = {};
-  float sbk_nx = 1.f;
+  float sbk_nx = 1.f, sbu_nx = 1.f;
   auto promote = [&](int i, int j) {
+    const float s = GLU && j >= kTN / 2 ? scu[i] : sc[i];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(pp[i][r], sc[i], acc[i][j][r]);
+    for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(pp[i][r], s, acc[i][j][r]);
   };
-  auto load_sc = [&](int i) { sc[i] = sa_nx[i] * sbk_nx; };
+  auto load_sc = [&](int i) {
+    sc[i] = sa_nx[i] * sbk_nx;
+    if (GLU) scu[i] = sa_nx[i] * sbu_nx;
+  };
+  // the block scales of chunk kb
+  auto rd_sbk = [&](int kb) {
+    sbk_nx = sbk_all[(GLU ? 0 : wc * kMaxChunks) + kb];
+    if (GLU) sbu_nx = sbk_all[kMaxChunks + kb];
+  };
   auto mfma = [&](const v8i& x, const v8i& y) -> v4f {  // B first
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(y, x, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
   };
@@ -666,7 +703,7 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
   // loads as in k_gemm_fp8: waves 0-3 the first half, 4-7 the second); A(0),
   // B(0), A(1), B(1) in flight in that order; chunk 0 published
   {
-    const float* psb = sbp + (int64_t)(tc.n0 / 128 + wc) * p.sb_rs;
+    const float* psb = sbp + (GLU ? b0 / 128 : (int64_t)(tc.n0 / 128 + wc)) * p.sb_rs;
     const __amdgpu_buffer_rsrc_t rK = make_rsrc(psb, (uint32_t)(((int64_t)(nk - 1) * p.sb_cs + 1) * 4));
     for (int r = 0; r * 256 < nk; ++r)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rK, (lds_ptr)(sbk_all + wc * kMaxChunks + r * 256 + wr * 64), 4,
@@ -692,7 +729,7 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
     pp[i] = v4f{0.f, 0.f, 0.f, 0.f};
   }
   bring[0] = rdB(sb0, 0);
-  sbk_nx = sbk_all[wc * kMaxChunks];
+  rd_sbk(0);
 #pragma unroll
   for (int i = 0; i < kTM; ++i) load_sc(i);
 
@@ -731,7 +768,7 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
           a[i] = rdA(anxt, i);
           if (i == 0) {
             rdSa(min(c + 1, nk - 1), sa_nx);
-            sbk_nx = sbk_all[wc * kMaxChunks + min(c + 1, nk - 1)];
+            rd_sbk(min(c + 1, nk - 1));
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -768,7 +805,25 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
   __builtin_amdgcn_s_barrier();
   fence();
   uint8_t* const ep = (w >> 1) == 0 ? sa0 : (w >> 1) == 1 ? sa1 : (w >> 1) == 2 ? sb0 : sb1;
-  if constexpr (QO) {
+  if constexpr (EPI == kEpiSwiglu) {
+    static_assert(!OUT_F32, "gated block: BF16 outputs only");
+    float gate[kTM][kTN / 2][4], up[kTM][kTN / 2][4];
+#pragma unroll
+    for (int i = 0; i < kTM; ++i)
+#pragma unroll
+      for (int j = 0; j < kTN / 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          gate[i][j][r] = acc[i][j][r];
+          up[i][j][r] = acc[i][j + kTN / 2][r];
+        }
+    // (the block scales in LDS are not needed any more: room for the row maxima)
+    store_tile_swiglu<kTM, 32>(gate, up, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 64, lane, sbk_all,
+                               wr * 64, wc);
+  } else if constexpr (EPI == kEpiDSwiglu) {
+    static_assert(!OUT_F32, "gated block's gradient: BF16 Dgrad only");
+    store_tile_dswiglu<kTM, kTN>(acc, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 128, lane);
+  } else if constexpr (EPI == kEpiQuant) {
     static_assert(!OUT_F32 && !GROUPED, "fused output quantization: BF16 Fprop/Dgrad only");
     store_tile_q<kTM, kTN, 32>(acc, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 128, lane);
   } else {
@@ -1009,14 +1064,14 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide_row(GemmArgs p) {
 namespace {
 
 template <int SB_MODE, int OUT_F32, bool GROUPED, bool KG = false, bool SC4 = false, bool EX = false,
-          bool QO = false, int INTV = 1>
+          int EPI = kEpiStore, int INTV = 1>
 hipError_t launch_one(const GemmArgs& a, hipStream_t st) {
   const int64_t tiles_n = a.N / kBN, tiles_m = (a.M + kBM - 1) / kBM;
   const int64_t tiles = KG ? a.E * 8 * ((tiles_m * tiles_n + 7) / 8)  // every expert: 8 XCD shares
                         : GROUPED ? (tiles_m + a.E) * tiles_n             // upper bound: a partial tile per expert
                                   : tiles_m * tiles_n;
   if (tiles <= 0) return hipSuccess;
-  hipLaunchKernelGGL((k_gemm_fp8<SB_MODE, OUT_F32, GROUPED, KG, SC4, EX, QO, INTV>), dim3((uint32_t)tiles), dim3(kNT),
+  hipLaunchKernelGGL((k_gemm_fp8<SB_MODE, OUT_F32, GROUPED, KG, SC4, EX, EPI, INTV>), dim3((uint32_t)tiles), dim3(kNT),
                      0, st, a);
   return hipGetLastError();
 }
@@ -1043,8 +1098,8 @@ static hipError_t launch_exact(const GemmArgs& a, hipStream_t st) {
   const bool sc4 = a.ld_sa % 4 == 0 && (reinterpret_cast<uintptr_t>(a.sa) & 15) == 0;
   const bool g = a.offsets != nullptr;
   if (a.qo != nullptr)  // fused output quantization (BF16 Fprop / Dgrad)
-    return sc4 ? launch_one<kSbBlock, 0, false, false, true, true, true>(a, st)
-               : launch_one<kSbBlock, 0, false, false, false, true, true>(a, st);
+    return sc4 ? launch_one<kSbBlock, 0, false, false, true, true, kEpiQuant>(a, st)
+               : launch_one<kSbBlock, 0, false, false, false, true, kEpiQuant>(a, st);
   if (a.sb_mode == kSbRow) return launch_one<kSbRow, 1, false, false, false, true>(a, st);
   if (sc4) {
     if (g) return a.out_f32 ? launch_one<kSbBlock, 1, true, false, true, true>(a, st)
@@ -1067,17 +1122,46 @@ hipError_t launch_gemm(const GemmArgs& a, hipStream_t st) {
 // matrix instruction over `chunks` chunks (0: the whole contraction).
 hipError_t launch_gemm_interval(const GemmArgs& a, int chunks, hipStream_t st) {
   switch (chunks) {
-    case 1: return launch_one<kSbBlock, 1, false, false, true, false, false, 1>(a, st);
-    case 2: return launch_one<kSbBlock, 1, false, false, true, false, false, 2>(a, st);
-    case 4: return launch_one<kSbBlock, 1, false, false, true, false, false, 4>(a, st);
-    case 8: return launch_one<kSbBlock, 1, false, false, true, false, false, 8>(a, st);
-    case 0: return launch_one<kSbBlock, 1, false, false, true, false, false, 0>(a, st);
+    case 1: return launch_one<kSbBlock, 1, false, false, true, false, kEpiStore, 1>(a, st);
+    case 2: return launch_one<kSbBlock, 1, false, false, true, false, kEpiStore, 2>(a, st);
+    case 4: return launch_one<kSbBlock, 1, false, false, true, false, kEpiStore, 4>(a, st);
+    case 8: return launch_one<kSbBlock, 1, false, false, true, false, kEpiStore, 8>(a, st);
+    case 0: return launch_one<kSbBlock, 1, false, false, true, false, kEpiStore, 0>(a, st);
     default: return hipErrorInvalidValue;
   }
 }
 
+// The gated feed-forward block: gate, up and their product in one kernel, and
+// the gradient's Dgrad with the block's derivative as its epilogue.
+static hipError_t launch_gated(const GemmArgs& a, bool sc4, hipStream_t st) {
+  const bool grouped = a.offsets != nullptr;
+  const int64_t tm = (a.M + kBM - 1) / kBM + (grouped ? a.E : 0);  // grouped: upper bound
+  if (a.gated == kSwiglu) {
+    const dim3 grid((uint32_t)(tm * (a.N / (kWBN / 2))));
+    if (grouped) {
+      if (sc4) hipLaunchKernelGGL((k_gemm_fp8_wide<0, true, kEpiSwiglu, true>), grid, dim3(kWNT), 0, st, a);
+      else hipLaunchKernelGGL((k_gemm_fp8_wide<0, true, kEpiSwiglu, false>), grid, dim3(kWNT), 0, st, a);
+    } else {
+      if (sc4) hipLaunchKernelGGL((k_gemm_fp8_wide<0, false, kEpiSwiglu, true>), grid, dim3(kWNT), 0, st, a);
+      else hipLaunchKernelGGL((k_gemm_fp8_wide<0, false, kEpiSwiglu, false>), grid, dim3(kWNT), 0, st, a);
+    }
+    return hipGetLastError();
+  }
+  if (sc4 && use_wide_tile(a)) {
+    const dim3 grid((uint32_t)(tm * (a.N / kWBN)));
+    if (grouped) hipLaunchKernelGGL((k_gemm_fp8_wide<0, true, kEpiDSwiglu>), grid, dim3(kWNT), 0, st, a);
+    else hipLaunchKernelGGL((k_gemm_fp8_wide<0, false, kEpiDSwiglu>), grid, dim3(kWNT), 0, st, a);
+    return hipGetLastError();
+  }
+  if (grouped) return sc4 ? launch_one<kSbBlock, 0, true, false, true, false, kEpiDSwiglu>(a, st)
+                          : launch_one<kSbBlock, 0, true, false, false, false, kEpiDSwiglu>(a, st);
+  return sc4 ? launch_one<kSbBlock, 0, false, false, true, false, kEpiDSwiglu>(a, st)
+             : launch_one<kSbBlock, 0, false, false, false, false, kEpiDSwiglu>(a, st);
+}
+
 hipError_t launch_gemm_fp8(const GemmArgs& a, hipStream_t st) {
   const bool sc4 = a.ld_sa % 4 == 0 && (reinterpret_cast<uintptr_t>(a.sa) & 15) == 0;
+  if (a.gated != kNotGated) return launch_gated(a, sc4, st);
   if (a.sb_mode == kSbRow) {  // weight gradients: FP32 out (row scales 128 B per row: no gain from blocks)
     if (use_wide_tile(a)) {
       const int64_t tn = a.N / kWBN, tm = (a.M + kBM - 1) / kBM;
@@ -1093,23 +1177,23 @@ hipError_t launch_gemm_fp8(const GemmArgs& a, hipStream_t st) {
   }
   if (a.qo != nullptr) {  // fused output quantization (BF16 Fprop / Dgrad)
     if (sc4 && use_wide_tile(a)) {
-      hipLaunchKernelGGL((k_gemm_fp8_wide<0, false, true>), dim3((uint32_t)(((a.M + kBM - 1) / kBM) * (a.N / kWBN))),
+      hipLaunchKernelGGL((k_gemm_fp8_wide<0, false, kEpiQuant>), dim3((uint32_t)(((a.M + kBM - 1) / kBM) * (a.N / kWBN))),
                          dim3(kWNT), 0, st, a);
       return hipGetLastError();
     }
-    return sc4 ? launch_one<kSbBlock, 0, false, false, true, false, true>(a, st)
-               : launch_one<kSbBlock, 0, false, false, false, false, true>(a, st);
+    return sc4 ? launch_one<kSbBlock, 0, false, false, true, false, kEpiQuant>(a, st)
+               : launch_one<kSbBlock, 0, false, false, false, false, kEpiQuant>(a, st);
   }
   // the 256 x 256 tile when it leaves no more than half of the chip idle
   if (sc4 && !(a.out_f32 && a.offsets != nullptr) && use_wide_tile(a)) {  // no FP32-output grouped instantiation
     const int64_t tn = a.N / kWBN, tm = (a.M + kBM - 1) / kBM;
     const int64_t tiles = a.offsets != nullptr ? (tm + a.E) * tn : tm * tn;  // grouped: upper bound
     if (a.offsets != nullptr)
-      hipLaunchKernelGGL((k_gemm_fp8_wide<0, true, false>), dim3((uint32_t)tiles), dim3(kWNT), 0, st, a);
+      hipLaunchKernelGGL((k_gemm_fp8_wide<0, true, kEpiStore>), dim3((uint32_t)tiles), dim3(kWNT), 0, st, a);
     else if (a.out_f32)
-      hipLaunchKernelGGL((k_gemm_fp8_wide<1, false, false>), dim3((uint32_t)tiles), dim3(kWNT), 0, st, a);
+      hipLaunchKernelGGL((k_gemm_fp8_wide<1, false, kEpiStore>), dim3((uint32_t)tiles), dim3(kWNT), 0, st, a);
     else
-      hipLaunchKernelGGL((k_gemm_fp8_wide<0, false, false>), dim3((uint32_t)tiles), dim3(kWNT), 0, st, a);
+      hipLaunchKernelGGL((k_gemm_fp8_wide<0, false, kEpiStore>), dim3((uint32_t)tiles), dim3(kWNT), 0, st, a);
     return hipGetLastError();
   }
   // row scales in 16-byte blocks of 4 chunks when every scale row is 16-byte aligned

@@ -265,4 +265,181 @@ __device__ __forceinline__ void store_tile_q(const float (&acc)[TM][TN][4], uint
   }
 }
 
+// ---------------------------------------------------------------------------
+// Epilogues of the gated feed-forward block h = silu(g) u, silu(g) = g s with
+// s = 1 / (1 + exp(-g)).
+
+// By the exponential that cannot overflow, so that s keeps its relative accuracy
+// down to the least numbers (1 / (1 + exp(-g)) is 0 from g = -89 on).
+__device__ __forceinline__ float sigmoid_f32(float g) {
+  const float e = expf(-fabsf(g));
+  return (g < 0.f ? e : 1.f) / (1.f + e);
+}
+
+// One wave's gate and up accumulators of the same WM x 64 outputs (layout of
+// store_tile with TRL = 1): gate and up as they are to p.gu (BF16, up N columns
+// after gate) if given, h to p.C (BF16) if given, and h's codes and scales,
+// over the unrounded values, to p.qo and p.so if given.  A 128-column group's
+// two halves are held by two waves, which exchange their rows' max-abs through
+// `half_max` [2][256]: with p.qo every wave of the workgroup makes this call.
+// row_in_tile is the strip's first row in the tile, half the wave's half.
+template <int TM, int ER>
+__device__ __forceinline__ void store_tile_swiglu(float (&g)[TM][4][4], const float (&u)[TM][4][4], uint8_t* ep,
+                                                  const GemmArgs& p, int64_t row0, int64_t mend, int col0, int lane,
+                                                  float* half_max, int row_in_tile, int half) {
+  const int lg = lane >> 4, l16 = lane & 15;
+  auto staged = [] {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the staging area is read out
+    __builtin_amdgcn_wave_barrier();
+  };
+  GemmArgs o = p;
+  if (p.gu != nullptr) {
+    o.C = p.gu;
+    o.ldc = p.ld_gu;
+    store_tile<TM, 4, 0, ER, 0, true>(g, ep, o, row0, mend, col0, lane);
+    staged();
+    store_tile<TM, 4, 0, ER, 0, true>(u, ep, o, row0, mend, col0 + (int)p.N, lane);
+    staged();
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) g[i][j][r] = g[i][j][r] * sigmoid_f32(g[i][j][r]) * u[i][j][r];
+  if (p.C != nullptr) {
+    store_tile<TM, 4, 0, ER, 0, true>(g, ep, p, row0, mend, col0, lane);
+    staged();
+  }
+  if (p.qo == nullptr) return;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m = max(m, abs_bits(g[i][j][r]));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16));  // the row's other three lanes
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    if (lg == 0) half_max[half * 256 + row_in_tile + 16 * i + l16] = __uint_as_float(m);
+  }
+  __syncthreads();
+  constexpr int P = 64 + 16;  // padded LDS row pitch of the codes
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int rt = row_in_tile + 16 * i + l16;
+    float sc, inv;
+    group_scale(__builtin_fmaxf(half_max[rt], half_max[256 + rt]), sc, inv);
+    const int64_t row = row0 + 16 * i + l16;
+    if (half == 0 && lg == 0 && row < mend) p.so[row * p.ld_so + (col0 >> 7)] = sc;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint32_t*>(ep + (16 * i + l16) * P + 16 * j + 4 * lg) =
+          pack4_e4m3_grp(g[i][j][0] * inv, g[i][j][1] * inv, g[i][j][2] * inv, g[i][j][3] * inv);
+  }
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int it = 0; it < TM; ++it) {  // 16 rows of four 16-byte segments
+    const int rl = it * 16 + (lane >> 2), ch = lane & 3;
+    const int64_t row = row0 + rl;
+    if (row >= mend) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(ep + rl * P + 16 * ch);
+    st_stream16<0>(p.qo + row * p.ld_qo + col0 + 16 * ch, v.x, v.y, v.z, v.w);
+  }
+}
+
+// The gradient's: the accumulators are dh (the output projection's Dgrad), g and
+// u come from p.gu, and
+//   dg = dh u (s + g s (1 - s)),   du = dh g s
+// go to p.C [M, 2N] (BF16, du N columns after dg) and h = g s u to p.h if given.
+// g and u are read, and all outputs written, as full 16-byte row segments
+// through the wave's staging area, one 16-row sub-tile at a time.
+template <int TM, int TN>
+__device__ __forceinline__ void store_tile_dswiglu(const float (&dh)[TM][TN][4], uint8_t* ep, const GemmArgs& p,
+                                                   int64_t row0, int64_t mend, int col0, int lane) {
+  constexpr int WN = 16 * TN;
+  constexpr int P = WN * 2 + 16;        // padded LDS row pitch of 16 rows of BF16
+  constexpr int CPR = WN * 2 / 16;      // 16-byte segments per row
+  constexpr int RPI = 64 / CPR;         // rows per load or store instruction
+  static_assert(2 * 16 * P <= 12288, "two staged sub-tiles fit a wave's staging area");
+  const int lg = lane >> 4, l16 = lane & 15;
+  uint8_t *const eg = ep, *const eu = ep + 16 * P;
+  auto lds_done = [] {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_wave_barrier();
+  };
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t rfirst = row0 + 16 * i;
+    if (rfirst >= mend) return;
+    if (i) lds_done();
+#pragma unroll
+    for (int it = 0; it < 16 / RPI; ++it) {
+      const int rl = it * RPI + lane / CPR, ch = lane % CPR;
+      const int64_t row = rfirst + rl;
+      uint4 vg = {0, 0, 0, 0}, vu = {0, 0, 0, 0};
+      if (row < mend) {
+        const uint16_t* src = p.gu + row * p.ld_gu + col0 + 8 * ch;
+        vg = *reinterpret_cast<const uint4*>(src);
+        vu = *reinterpret_cast<const uint4*>(src + p.N);
+      }
+      *reinterpret_cast<uint4*>(eg + rl * P + 16 * ch) = vg;
+      *reinterpret_cast<uint4*>(eu + rl * P + 16 * ch) = vu;
+    }
+    lds_done();
+    uint2 hs[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      uint2* const pg = reinterpret_cast<uint2*>(eg + l16 * P + 2 * (16 * j + 4 * lg));
+      uint2* const pu = reinterpret_cast<uint2*>(eu + l16 * P + 2 * (16 * j + 4 * lg));
+      const uint2 wg = *pg, wu = *pu;
+      float dg[4], du[4], h[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t bg = r < 2 ? wg.x : wg.y, bu = r < 2 ? wu.x : wu.y;
+        const float g = __uint_as_float(r & 1 ? bg & 0xFFFF0000u : bg << 16);
+        const float u = __uint_as_float(r & 1 ? bu & 0xFFFF0000u : bu << 16);
+        const float s = sigmoid_f32(g), gs = g * s, d = dh[i][j][r];
+        dg[r] = d * u * __builtin_fmaf(gs, 1.f - s, s);
+        du[r] = d * gs;
+        h[r] = gs * u;
+      }
+      auto pack = [](const float (&v)[4]) {
+        return make_uint2(f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
+                          f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16));
+      };
+      *pg = pack(dg);
+      *pu = pack(du);
+      hs[j] = pack(h);
+    }
+    lds_done();
+    uint16_t* const C = reinterpret_cast<uint16_t*>(p.C);
+#pragma unroll
+    for (int it = 0; it < 16 / RPI; ++it) {
+      const int rl = it * RPI + lane / CPR, ch = lane % CPR;
+      const int64_t row = rfirst + rl;
+      if (row >= mend) continue;
+      const uint4 vg = *reinterpret_cast<const uint4*>(eg + rl * P + 16 * ch);
+      const uint4 vu = *reinterpret_cast<const uint4*>(eu + rl * P + 16 * ch);
+      uint16_t* dst = C + row * p.ldc + col0 + 8 * ch;
+      st_stream16<0>(dst, vg.x, vg.y, vg.z, vg.w);
+      st_stream16<0>(dst + p.N, vu.x, vu.y, vu.z, vu.w);
+    }
+    if (p.h == nullptr) continue;
+    lds_done();
+#pragma unroll
+    for (int j = 0; j < TN; ++j) *reinterpret_cast<uint2*>(eg + l16 * P + 2 * (16 * j + 4 * lg)) = hs[j];
+    lds_done();
+#pragma unroll
+    for (int it = 0; it < 16 / RPI; ++it) {
+      const int rl = it * RPI + lane / CPR, ch = lane % CPR;
+      const int64_t row = rfirst + rl;
+      if (row >= mend) continue;
+      const uint4 v = *reinterpret_cast<const uint4*>(eg + rl * P + 16 * ch);
+      st_stream16<0>(p.h + row * p.ld_h + col0 + 8 * ch, v.x, v.y, v.z, v.w);
+    }
+  }
+}
+
 }  // namespace fp8q

@@ -58,6 +58,9 @@ enum SbMode : int {
   kSbRow = 1     // one scale per output column per chunk:      sb[n*sb_rs + kb]
 };
 
+// What a product's epilogue makes of it for a gated feed-forward block.
+enum GatedMode : int { kNotGated = 0, kSwiglu = 1, kDSwiglu = 2 };
+
 // C[m, n] = sum_kb P_kb[m, n] * sa[m*ld_sa + kb] * sB(n, kb), P_kb the FP8
 // product of the 128-long chunk kb of A[m, :] and B[n, :] (both row-major
 // with the contraction axis contiguous).
@@ -88,6 +91,15 @@ struct GemmArgs {
   uint8_t* qo;
   float* so;
   int64_t ld_qo, ld_so;
+  // gated block: kSwiglu computes h = silu(g) u from gate g and up u, B's
+  // rows [0, N) and [N, 2N) (scales likewise), to C (BF16) and / or qo, so;
+  // kDSwiglu takes its own product as dh and gu as g and u, and writes
+  // their gradients to C [M, 2N] and, if h is given, h again
+  int gated;            // GatedMode
+  uint16_t* gu;         // [M, 2N] BF16: optional output (SWIGLU), input (DSWIGLU)
+  int64_t ld_gu;
+  uint16_t* h;          // [M, N] BF16, optional (DSWIGLU)
+  int64_t ld_h;
 };
 
 hipError_t launch_gemm(const GemmArgs& a, hipStream_t st);
@@ -103,6 +115,11 @@ hipError_t launch_gemm_fp8(const GemmArgs& a, hipStream_t st);
 // the promotion-interval study (block scales, FP32 output): partials chained
 // through the matrix instruction over `chunks` chunks (1, 2, 4, 8; 0 = all)
 hipError_t launch_gemm_interval(const GemmArgs& a, int chunks, hipStream_t st);
+
+// The gated block of at most kFewRows rows (a.gated == kSwiglu, dense); hf: room
+// for h in FP32 [M, N], needed where codes are wanted.
+constexpr int kFewRows = 64;
+hipError_t launch_swiglu_few(const GemmArgs& a, float* hf, hipStream_t st);
 
 // Microscaling (MXFP8 E4M3) quantizers: one E8M0 scale byte per 32
 // consecutive elements, along rows (quant_mx) or along columns with the
@@ -198,5 +215,58 @@ typedef ClipTable<kMaxClipTensors> ClipBatch;
 hipError_t launch_grad_sumsq(const ClipBatch& b, ClipBatch* table, double* part, int* held, hipStream_t st);
 hipError_t launch_grad_scale(const ClipBatch* table, int chunks, bool out_bf16, const double* part, int parts,
                              double max_norm, float* norm, hipStream_t st);
+
+// -------------------------------------------------------------- RMS norm
+constexpr int64_t kMaxNormCols = 16384;  // a row stays in a block's registers
+// What forward and gradient share: the rows' shape and type, the weights, and
+// the outputs (out: y or dx; out or q may be NULL).
+struct NormRows {
+  bool bf16;
+  int64_t rows, cols;
+  const float* w;
+  void* out;
+  int64_t ld_out;
+  uint8_t* q;
+  int64_t ld_q;
+  float* s;
+  int64_t ld_s;
+};
+hipError_t launch_rms_norm(const NormRows& a, const void* x, int64_t ld_x, const void* res, int64_t ld_res, float eps,
+                           void* sum, int64_t ld_sum, float* rstd, hipStream_t st);
+// Blocks of the gradient's launch, each of which leaves a row of cols partial
+// sums of dw.
+int64_t rms_norm_parts(int64_t rows, int64_t cols);
+hipError_t launch_rms_norm_bwd(const NormRows& a, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                               const float* rstd, const void* dsum, int64_t ld_dsum, float* part, float* dw,
+                               hipStream_t st);
+
+// ---------------------------------------------------------------- AdamW
+constexpr int kMaxAdamTensors = 48;  // per launch: the table travels in the kernel's arguments
+constexpr int kAdamChunk = 8192;     // elements of one tensor a block takes at a time
+template <int N>
+struct AdamTable {
+  float* p[N];
+  const void* g[N];
+  void* m[N];
+  void* v[N];
+  float* m_scale[N];
+  float* v_scale[N];
+  uint16_t* copy[N];
+  int cum[N + 1];    // first chunk of each tensor, then their number
+  uint32_t key[N];   // of its random numbers
+  uint16_t last[N];  // elements of a tensor's last chunk
+  uint16_t n;
+};
+typedef AdamTable<kMaxAdamTensors> AdamBatch;
+struct AdamStep {
+  float beta1, rest1, beta2, rest2;  // rest = 1 - beta
+  float keep;                        // 1 - lr * weight decay
+  float step;                        // lr / (1 - beta1^t)
+  float root;                        // 1 / sqrt(1 - beta2^t)
+  float eps;
+  const float* norm;                 // of all gradients, or NULL
+  double max_norm;
+};
+hipError_t launch_adamw(const AdamBatch& b, const AdamStep& a, bool g_bf16, bool bits8, hipStream_t st);
 
 }  // namespace fp8q

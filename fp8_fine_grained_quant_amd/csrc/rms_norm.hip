@@ -1,0 +1,351 @@
+// Root-mean-square norm of rows, with the residual's addition in front of it
+// and 1x128 E4M3 codes behind it, and its gradient (gfx950).
+//
+//   t = x + residual (rounded to the rows' type: the stream as it is held)
+//   r = 1 / sqrt(mean(t^2) + eps),  y = t r w
+// and, from dy, t and r,
+//   a = dy w,  c = mean(a t r),  dt = r (a - t r c) (+ the stream's own gradient)
+//   dw = sum over the rows of dy t r
+// All arithmetic is FP32; y and dt are rounded once, to the rows' type or (over
+// the unrounded values' scales) to codes.
+//
+// Both are bound by memory, so a row is read once and stays in registers while
+// its sum is formed, and (up to 8192 columns) the weights stay in registers from
+// row to row: a block's threads own fixed columns and the block takes every
+// gridDim.x-th row.
+// The gradient's dw needs the same: each block sums its rows' part of it in
+// registers and writes it once, and a second launch adds the blocks' parts (in
+// a fixed order; no atomics).
+
+#include "launch.h"
+#include "row_io.h"
+
+#include <type_traits>
+
+namespace fp8q {
+
+namespace {
+
+// Threads per row and 8-column pieces per thread (V): see launch_norm.
+constexpr int kNormThreads1 = 1024, kNormThreads = 512;
+// Pieces whose weights stay in registers; with 4 a gradient's registers would spill.
+constexpr int kHeldPieces = 2;
+template <int V>
+constexpr int norm_threads() { return V == 1 ? kNormThreads1 : kNormThreads; }
+
+template <class Row>
+__device__ __forceinline__ int norm_col(int piece) { return (piece >> 4) * 128 + (piece & 15) * Row::kLen; }
+
+// The pointer, as one that the compiler has not loaded from before: values that
+// are read anew for every row are not to be kept in registers.
+__device__ __forceinline__ const float* again(const float* p) {
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
+// The weights of a lane's 8 columns, zeros past the row's end.
+template <class Row>
+__device__ __forceinline__ void load_weights(const float* w, int c0, int cols, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = Row::kRuns == 1 ? c0 + 4 * h : c0 + 64 * h;
+    u32x4 u = {0, 0, 0, 0};
+    if (c + 4 <= cols) {
+      u = ld16u<0>(w + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (c + e < cols) u[e] = __float_as_uint(w[c + e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[4 * h + e] = __uint_as_float(u[e]);
+  }
+}
+
+// A lane's 8 columns of a row, zeros in every column past the row's end.
+template <class Row, bool TINY, int NT>
+__device__ __forceinline__ typename Row::Raw load_row_piece(const typename Row::elem* p, int c0, int cols,
+                                                            bool whole) {
+  typename Row::Raw raw;
+  if (!TINY && whole) {
+    raw = load_piece<Row, true, false, NT>(p, c0, cols);
+#pragma unroll
+    for (int r = 0; r < Row::kRuns; ++r)
+      if (c0 + 64 * r >= cols) raw.a[r] = u32x4{0, 0, 0, 0};
+  } else {
+    raw = load_piece<Row, false, TINY, NT>(p, c0, cols);
+  }
+  return raw;
+}
+template <class Row, int NT>
+__device__ __forceinline__ void store_row_piece(typename Row::elem* p, int c0, int cols, bool whole,
+                                                const typename Row::Raw& raw) {
+  if (whole) store_piece<Row, true, NT>(p, c0, cols, raw);
+  else store_piece<Row, false, 0>(p, c0, cols, raw);
+}
+
+// Codes and scale of a lane's 8 FP32 values; 16 lanes hold a group.
+template <class Row>
+__device__ __forceinline__ void store_quantized(const float (&y)[8], uint8_t* q, float* s, int piece, int c0, int cols,
+                                                bool whole) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, abs_bits(y[e]));
+  float sc, inv;
+  group_scale(__uint_as_float(row16_max_u32(m)), sc, inv);
+  const uint32_t w0 = pack4_e4m3_grp(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+  const uint32_t w1 = pack4_e4m3_grp(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+  if (whole) store_codes<Row, true, 0>(q, c0, cols, w0, w1);
+  else store_codes<Row, false, 0>(q, c0, cols, w0, w1);
+  if ((piece & 15) == 0 && (piece >> 4) * 128 < cols) s[piece >> 4] = sc;
+}
+
+// Sum over the block, the same bits in every thread.  `red` holds a value of
+// each wave; the caller alternates between two of them, so that one barrier a
+// call is enough.
+__device__ __forceinline__ float norm_block_sum(float v, float* red) {
+  v = row16_sum(v);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  const int waves = (int)blockDim.x >> 6;
+  if (waves == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  // lane l of every 16 holds wave l's value
+  const int l = threadIdx.x & 15;
+  return row16_sum(l < waves ? red[l] : 0.f);
+}
+
+template <class Row, int V, bool TINY>
+__global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a, const void* x_, int64_t ld_x,
+                                                                 const void* res_, int64_t ld_res, float eps,
+                                                                 void* sum_, int64_t ld_sum, float* rstd_out) {
+  typedef typename Row::elem elem;
+  __shared__ float red[2][16];
+  const elem *x = (const elem*)x_, *res = (const elem*)res_;
+  elem *y = (elem*)a.out, *sum = (elem*)sum_;
+  const int cols = (int)a.cols;
+  int piece[V], c0[V];
+  bool whole[V];
+  float w[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    piece[i] = i * (int)blockDim.x + (int)threadIdx.x;
+    c0[i] = norm_col<Row>(piece[i]);
+    whole[i] = no_cut<Row>(c0[i], cols, cols);
+    if (V <= kHeldPieces) load_weights<Row>(a.w, c0[i], cols, w[i]);
+  }
+  const float inv_cols = 1.f / (float)cols;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+    typename Row::Raw raw[V], other[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) raw[i] = load_row_piece<Row, TINY, 0>(x + r * ld_x, c0[i], cols, whole[i]);
+    if (res)
+#pragma unroll
+      for (int i = 0; i < V; ++i) other[i] = load_row_piece<Row, TINY, 0>(res + r * ld_res, c0[i], cols, whole[i]);
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float v[8];
+      Row::unpack(raw[i], v);
+      if (res) {
+        float o[8];
+        Row::unpack(other[i], o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += o[e];
+        raw[i] = Row::pack(v);
+        Row::unpack(raw[i], v);
+        store_row_piece<Row, 0>(sum + r * ld_sum, c0[i], cols, whole[i], raw[i]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
+    }
+    ss = norm_block_sum(ss, red[turn]);
+    const float rstd = 1.f / sqrtf(__builtin_fmaf(ss, inv_cols, eps));
+    if (threadIdx.x == 0) rstd_out[r] = rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float v[8];
+      Row::unpack(raw[i], v);
+      if (V > kHeldPieces) load_weights<Row>(again(a.w), c0[i], cols, w[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * rstd * w[i][e];
+      if (y) store_row_piece<Row, 0>(y + r * a.ld_out, c0[i], cols, whole[i], Row::pack(v));
+      if (a.q) store_quantized<Row>(v, a.q + r * a.ld_q, a.s + r * a.ld_s, piece[i], c0[i], cols, whole[i]);
+    }
+  }
+}
+
+template <class Row, int V, bool TINY>
+__global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRows a, const void* dy_, int64_t ld_dy,
+                                                                     const void* x_, int64_t ld_x, const float* rstd_in,
+                                                                     const void* dsum_, int64_t ld_dsum,
+                                                                     float* __restrict__ part) {
+  typedef typename Row::elem elem;
+  __shared__ float red[2][16];
+  const elem *dy = (const elem*)dy_, *x = (const elem*)x_, *dsum = (const elem*)dsum_;
+  elem* dx = (elem*)a.out;
+  const int cols = (int)a.cols;
+  int piece[V], c0[V];
+  bool whole[V];
+  float w[V][8], dw[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    piece[i] = i * (int)blockDim.x + (int)threadIdx.x;
+    c0[i] = norm_col<Row>(piece[i]);
+    whole[i] = no_cut<Row>(c0[i], cols, cols);
+    if (V <= kHeldPieces) load_weights<Row>(a.w, c0[i], cols, w[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+  }
+  const float inv_cols = 1.f / (float)cols;
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+    typename Row::Raw rx[V], rd[V], ro[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      rx[i] = load_row_piece<Row, TINY, 0>(x + r * ld_x, c0[i], cols, whole[i]);
+      rd[i] = load_row_piece<Row, TINY, 0>(dy + r * ld_dy, c0[i], cols, whole[i]);
+    }
+    if (dsum)
+#pragma unroll
+      for (int i = 0; i < V; ++i) ro[i] = load_row_piece<Row, TINY, 0>(dsum + r * ld_dsum, c0[i], cols, whole[i]);
+    const float rstd = rstd_in[r];
+    float c = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float vx[8], vd[8];
+      Row::unpack(rx[i], vx);
+      Row::unpack(rd[i], vd);
+      if (V > kHeldPieces) load_weights<Row>(again(a.w), c0[i], cols, w[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = vd[e] * (vx[e] * rstd);
+        dw[i][e] += t;
+        c = __builtin_fmaf(t, w[i][e], c);
+      }
+    }
+    c = norm_block_sum(c, red[turn]) * inv_cols;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float vx[8], vd[8], vo[8];
+      Row::unpack(rx[i], vx);
+      Row::unpack(rd[i], vd);
+      if (dsum) Row::unpack(ro[i], vo);
+      if (V > kHeldPieces) load_weights<Row>(again(a.w), c0[i], cols, w[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float g = __builtin_fmaf(vx[e] * rstd, -c, vd[e] * w[i][e]) * rstd;
+        vd[e] = dsum ? g + vo[e] : g;
+      }
+      if (dx) store_row_piece<Row, 0>(dx + r * a.ld_out, c0[i], cols, whole[i], Row::pack(vd));
+      if (a.q) store_quantized<Row>(vd, a.q + r * a.ld_q, a.s + r * a.ld_s, piece[i], c0[i], cols, whole[i]);
+    }
+  }
+  part += (int64_t)blockIdx.x * cols;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = Row::kRuns == 1 ? c0[i] + 4 * h : c0[i] + 64 * h;
+      if (c + 4 <= cols) {
+        st16u<0>(part + c, u32x4{__float_as_uint(dw[i][4 * h]), __float_as_uint(dw[i][4 * h + 1]),
+                                 __float_as_uint(dw[i][4 * h + 2]), __float_as_uint(dw[i][4 * h + 3])});
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (c + e < cols) part[c + e] = dw[i][4 * h + e];
+      }
+    }
+}
+
+// dw[c] = the sum of the blocks' parts, 64 columns and 16 runs of parts a block.
+constexpr int kPartCols = 64, kPartRuns = 16;
+__global__ __launch_bounds__(kPartCols* kPartRuns) void k_norm_parts(const float* __restrict__ part, int parts,
+                                                                     int cols, float* __restrict__ dw) {
+  __shared__ float red[kPartRuns][kPartCols];
+  const int c = (int)blockIdx.x * kPartCols + (int)(threadIdx.x & (kPartCols - 1)), run = (int)threadIdx.x / kPartCols;
+  float s = 0.f;
+  if (c < cols)
+    for (int p = run; p < parts; p += kPartRuns) s += part[(int64_t)p * cols + c];
+  red[run][threadIdx.x & (kPartCols - 1)] = s;
+  __syncthreads();
+  if (run == 0 && c < cols) {
+#pragma unroll
+    for (int i = 1; i < kPartRuns; ++i) s += red[i][threadIdx.x & (kPartCols - 1)];
+    dw[c] = s;
+  }
+}
+
+struct NormShape {
+  int v, threads;
+};
+// Pieces of 8 columns, 16 to a group of 128.
+NormShape norm_shape(int64_t cols) {
+  const int64_t pieces = (cols + 127) / 128 * 16;
+  NormShape n;
+  n.v = pieces <= kNormThreads ? 1 : pieces <= 2 * kNormThreads ? 2 : 4;
+  n.threads = (int)((pieces + 64 * n.v - 1) / (64 * n.v) * 64);
+  return n;
+}
+
+// Blocks that fit the device at once (8 waves a SIMD are not reached at these
+// register counts; 2048 threads a compute unit keep enough loads in flight).
+int64_t norm_blocks(int64_t rows, int threads, int per_cu_threads) {
+  const int64_t most = (int64_t)device_cu_count() * (per_cu_threads / threads < 1 ? 1 : per_cu_threads / threads);
+  return rows < most ? rows : most;
+}
+
+// fn(Row type, pieces per thread, a row may be shorter than a lane's run)
+template <class F>
+hipError_t norm_dispatch(bool bf16, int64_t cols, int v, F fn) {
+  auto with = [&](auto row) {
+    typedef decltype(row) Row;
+    if (cols < Row::kLen) return fn(row, std::integral_constant<int, 1>{}, std::true_type{});
+    switch (v) {
+      case 1: return fn(row, std::integral_constant<int, 1>{}, std::false_type{});
+      case 2: return fn(row, std::integral_constant<int, 2>{}, std::false_type{});
+      default: return fn(row, std::integral_constant<int, 4>{}, std::false_type{});
+    }
+  };
+  return bf16 ? with(RowBF16{}) : with(RowF32{});
+}
+
+}  // namespace
+
+static_assert(4 * kNormThreads * 8 == kMaxNormCols, "the longest row");
+
+hipError_t launch_rms_norm(const NormRows& a, const void* x, int64_t ld_x, const void* res, int64_t ld_res, float eps,
+                           void* sum, int64_t ld_sum, float* rstd, hipStream_t st) {
+  const NormShape n = norm_shape(a.cols);
+  const int64_t blocks = norm_blocks(a.rows, n.threads, 2048);
+  return norm_dispatch(a.bf16, a.cols, n.v, [&](auto row, auto v, auto tiny) {
+    hipLaunchKernelGGL((k_rms_norm<decltype(row), decltype(v)::value, decltype(tiny)::value>), dim3((uint32_t)blocks),
+                       dim3(n.threads), 0, st, a, x, ld_x, res, ld_res, eps, sum, ld_sum, rstd);
+    return hipGetLastError();
+  });
+}
+
+int64_t rms_norm_parts(int64_t rows, int64_t cols) { return norm_blocks(rows, norm_shape(cols).threads, 1024); }
+
+hipError_t launch_rms_norm_bwd(const NormRows& a, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                               const float* rstd, const void* dsum, int64_t ld_dsum, float* part, float* dw,
+                               hipStream_t st) {
+  const NormShape n = norm_shape(a.cols);
+  const int64_t parts = rms_norm_parts(a.rows, a.cols);
+  if (parts > 0) {
+    const hipError_t err = norm_dispatch(a.bf16, a.cols, n.v, [&](auto row, auto v, auto tiny) {
+      hipLaunchKernelGGL((k_rms_norm_bwd<decltype(row), decltype(v)::value, decltype(tiny)::value>),
+                         dim3((uint32_t)parts), dim3(n.threads), 0, st, a, dy, ld_dy, x, ld_x, rstd, dsum, ld_dsum,
+                         part);
+      return hipGetLastError();
+    });
+    if (err != hipSuccess) return err;
+  }
+  hipLaunchKernelGGL(k_norm_parts, dim3((uint32_t)((a.cols + kPartCols - 1) / kPartCols)), dim3(kPartCols * kPartRuns),
+                     0, st, part, (int)parts, (int)a.cols, dw);
+  return hipGetLastError();
+}
+
+}  // namespace fp8q

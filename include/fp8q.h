@@ -642,6 +642,153 @@ fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, dou
 /* Bytes of workspace that call needs (-1: n out of range). */
 int64_t fp8q_grad_clip_workspace(int64_t n);
 
+/*
+ * ---- A training block around the products: norm, gated feed-forward block,
+ * optimizer step.
+ *
+ * Root-mean-square norm of token rows, with the residual's addition before it:
+ *   t = x + residual (FP32, rounded to the rows' type; x itself without one)
+ *   rstd = 1 / sqrt(mean(t^2) + eps),  y = t * rstd * weight
+ *   x, residual : [rows, cols] of type t, row strides ld_x, ld_r; residual NULL:
+ *                 none (then sum is not used)
+ *   weight : [cols] FP32;  eps >= 0, finite
+ *   y      : [rows, cols] of type t, or NULL
+ *   q, scale : [rows, cols] codes and [rows, ceil(cols/128)] scales of y as it
+ *            is in FP32, before its rounding to t (one rounding, as an activation
+ *            that is quantized where it is computed), or NULL.  At least one of
+ *            y and q is wanted.
+ *   sum    : [rows, cols] of type t: t, the stream that goes on (may be x or
+ *            residual itself)
+ *   rstd   : [rows] FP32, for the gradient
+ * Rows start at any element and have any stride, as those of the routing entry
+ * points; cols <= 16384.  Squares are summed in FP32: a row's sum of squares
+ * has to be finite there.  With eps = 0 a row of zeros gives NaN.
+ */
+fp8q_status fp8q_rms_norm(const void* x, fp8q_dtype t, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                          int64_t ld_r, const float* weight, float eps, void* y, int64_t ld_y, uint8_t* q, int64_t ld_q,
+                          float* scale, int64_t ld_s, void* sum, int64_t ld_sum, float* rstd, hipStream_t stream);
+
+/*
+ * Its gradient.  With h = x * rstd (x: what was normalized, the sum where there
+ * was a residual) and a = dy * weight:
+ *   dx = rstd * (a - h * mean(a * h)) + dsum,   dweight = sum over rows of dy * h
+ *   dsum    : [rows, cols] of type t, the gradient of the stream that went on, or
+ *             NULL; dx is the gradient of x and of residual alike
+ *   dx      : [rows, cols] of type t, or NULL (dx may be dy, x or dsum itself)
+ *   q, scale : codes and scales of dx before its rounding to t, or NULL
+ *   dweight : [cols] FP32, zeros for rows = 0
+ *   workspace : 4-byte aligned, fp8q_rms_norm_bwd_workspace(rows, cols) bytes on
+ *             the current device
+ * Rows' contributions to dweight are added in an order that depends on the sizes
+ * and the device alone.
+ */
+fp8q_status fp8q_rms_norm_bwd(const void* dy, const void* x, fp8q_dtype t, int64_t rows, int64_t cols, int64_t ld_dy,
+                              int64_t ld_x, const float* weight, const float* rstd, const void* dsum, int64_t ld_dsum,
+                              void* dx, int64_t ld_dx, uint8_t* q, int64_t ld_q, float* scale, int64_t ld_s,
+                              float* dweight, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+/* Bytes of workspace that call needs (-1: sizes out of range). */
+int64_t fp8q_rms_norm_bwd_workspace(int64_t rows, int64_t cols);
+
+/*
+ * Gated feed-forward block: both projections, the activation and the product in
+ * one kernel,
+ *   g = X Wg^T,  u = X Wu^T,  h = silu(g) * u,  silu(g) = g / (1 + exp(-g))
+ * from FP32 g and u, with the operands of fp8q_gemm_fprop for the stacked weight:
+ *   xq, xs : [M, K] codes, [M, K/128] scales (contiguous)
+ *   wq, ws : [2N, K] codes, [2N/128, K/128] block scales (contiguous): rows
+ *            [0, N) are Wg, rows [N, 2N) Wu
+ *   h      : [M, N] BF16, or NULL
+ *   gu     : [M, 2N] BF16: g and u beside each other, for the gradient, or NULL
+ *   q, scale : [M, N] codes and [M, N/128] scales of h as it is in FP32, before
+ *            its rounding to BF16, or NULL.  One of h, gu and q at least.
+ *   workspace : 16-byte aligned, fp8q_gemm_swiglu_workspace(M, N, q wanted) bytes
+ * More than 64 rows have the accuracy of fp8q_gemm_fprop in g and u; up to 64
+ * rows run on a kernel for few rows with that of fp8q_gemm_fprop_exact.
+ * Rules: N % 128 == 0, K % 128 == 0, K <= 131072, any M >= 0; xq, wq, h, gu, q
+ * 16-byte aligned with row strides that are multiples of 16 bytes.
+ */
+fp8q_status fp8q_gemm_swiglu(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t M,
+                             int64_t N, int64_t K, void* h, int64_t ld_h, void* gu, int64_t ld_gu, uint8_t* q,
+                             int64_t ld_q, float* scale, int64_t ld_s, void* workspace, int64_t workspace_bytes,
+                             hipStream_t stream);
+/* Bytes of workspace that call needs (-1: sizes out of range). */
+int64_t fp8q_gemm_swiglu_workspace(int64_t M, int64_t N, int codes);
+
+/*
+ * The same by expert: rows [o_e, o_{e+1}) use the expert's own wq [E, 2N, K] and
+ * ws [E, 2N/128, K/128]; offsets as for fp8q_grouped_gemm.  No workspace.
+ */
+fp8q_status fp8q_grouped_gemm_swiglu(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                                     const int32_t* offsets, int64_t E, int64_t M_total, int64_t N, int64_t K, void* h,
+                                     int64_t ld_h, void* gu, int64_t ld_gu, uint8_t* q, int64_t ld_q, float* scale,
+                                     int64_t ld_s, hipStream_t stream);
+
+/*
+ * Gradient of gate and up: the Dgrad of the output projection (dh, which stays in
+ * FP32) with the block's derivative in its epilogue, s = 1 / (1 + exp(-g)):
+ *   dh = dY W,  dg = dh u (s + g s (1 - s)),  du = dh g s,  h = g s u
+ *   dyq, dys, wq_t, ws, M, N, K : as for fp8q_gemm_dgrad: W is the output
+ *            projection [N, K], K the block's width
+ *   gu     : [M, 2K] BF16, what fp8q_gemm_swiglu left
+ *   dgu    : [M, 2K] BF16: dg and du beside each other (may be gu itself)
+ *   h      : [M, K] BF16, for the output projection's weight gradient, or NULL
+ * From dgu, fp8q_gemm_dgrad on the stacked weight's transposed codes and
+ * fp8q_gemm_wgrad make dX and the stacked weight's gradient.
+ */
+fp8q_status fp8q_gemm_dgrad_swiglu(const uint8_t* dyq, const float* dys, const uint8_t* wq_t, const float* ws,
+                                   int64_t M, int64_t N, int64_t K, const void* gu, int64_t ld_gu, void* dgu,
+                                   int64_t ld_dgu, void* h, int64_t ld_h, hipStream_t stream);
+
+/* The same by expert, with the operands and rules of fp8q_grouped_gemm_dgrad. */
+fp8q_status fp8q_grouped_gemm_dgrad_swiglu(const uint8_t* dyq, const float* dys, const uint8_t* wq_t, const float* ws,
+                                           const int32_t* offsets, int64_t E, int64_t M_total, int64_t N, int64_t K,
+                                           const void* gu, int64_t ld_gu, void* dgu, int64_t ld_dgu, void* h,
+                                           int64_t ld_h, hipStream_t stream);
+
+/*
+ * One AdamW step (number `step`, from 1 on) of n tensors, in place and in FP32:
+ *   g' = g * c,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr weight_decay) - lr m / (1 - beta1^step) / (sqrt(v / (1 - beta2^step)) + eps)
+ *   tensors : HOST array (read during the call only); per tensor of len elements
+ *     p       FP32 parameters
+ *     g       gradients of type gt
+ *     m, v    bits = 32: FP32 states.  bits = 8: E4M3 codes of m and of sqrt(v),
+ *             with one FP32 scale (m_scale, v_scale: [ceil(len/128)]) per 128
+ *             elements; zeros in both are a new state
+ *     copy    BF16 copies of the new parameters, or NULL
+ *   norm, max_norm : norm (one FP32 on the device, as fp8q_grad_clip leaves it):
+ *             c = 1 if norm <= max_norm, else max_norm / norm, which and whose
+ *             product with g are in 64 bits as there; NULL: c = 1
+ * bits = 8: the step uses m and v in FP32 and rounds them behind it, scale =
+ * fl32(max(amax, 2^-100) / 448), y = x * fl32(448 / max(amax, 2^-100)), to one of
+ * the two E4M3 values around y: away from zero where floor(t + u) > floor(t), t = |y|
+ * in steps of E4M3 there, u in [0, 1) of 16 random bits, the lower ones of the
+ * element's 32 for m, the upper ones for sqrt(v).  sqrt(v) > 0 is never rounded to
+ * 0.  The bits are mix(i_lo * 0x85297A4D + i_hi * 0x27D4EB2F + key) of the element's
+ * place i in its tensor, key = mix(mix(seed_lo + 0x9E3779B1 * tensor) + seed_hi),
+ * where mix(x) in 32 bits is x = (x ^ x >> 16) * 0x6C8E9CF5, x = (x ^ x >> 15) *
+ * 0xB2D05E13, x ^ x >> 16: the same seed repeats a step, another one for every step
+ * keeps the roundings independent.  A gradient that is not finite makes its group
+ * of 128 states NaN.
+ * 0 <= beta < 1, eps >= 0, max_norm >= 0 (inf: no clipping).  Tensors start at any
+ * element and must not overlap each other (parameters that do are refused,
+ * FP8Q_ERR_SHAPE).  The numbers of the step are read at the call: a captured call
+ * repeats the same step.
+ */
+typedef struct {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  uint16_t* copy;
+  int64_t len;
+} fp8q_adamw_tensor;
+fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int64_t n, fp8q_dtype gt, int bits, double lr, double beta1,
+                       double beta2, double eps, double weight_decay, int64_t step, uint64_t seed, const float* norm,
+                       double max_norm, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
