@@ -426,10 +426,7 @@ def library_swiglu(fq, s):
 
 
 def library_adamw(fq, s):
-    held = s["m"], s["v"]
-    if s["scales"]:
-        held = tuple([as_codes(q) for q in h] for h in held)
-    fq.adamw(s["p"], s["g"], *held, scales=s["scales"], copies=s["copies"], norm=s["norm"], max_norm=s["max_norm"],
+    fq.adamw(s["p"], s["g"], s["m"], s["v"], scales=s["scales"], copies=s["copies"], norm=s["norm"], max_norm=s["max_norm"],
              **s["step"])
     return s["flat"]
 
