@@ -1123,8 +1123,8 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.95), eps=1
           seed=0, norm=None, max_norm=float("inf"), copies=None, stream=None):
     """One AdamW step (number `step`, from 1 on) of FP32 params, in place.
     grads: FP32 or BF16.  exp_avg, exp_avg_sq: FP32, or with scales (two lists
-    of FP32 [ceil(n / 128)]) the E4M3 codes of the first moment and of the
-    second one's root, rounded at random by `seed` (another one for every
+    of FP32 [ceil(n / 128)]) the E4M3 codes (uint8, or torch's float8_e4m3fn) of
+    the first moment and of the second one's root, rounded at random by `seed` (another one for every
     step).  norm: the gradients' norm (0-dim FP32 on the GPU, from grad_clip with
     max_norm=inf), by which the step clips them to max_norm.  copies: BF16
     tensors that receive the new parameters."""

@@ -135,7 +135,8 @@ __device__ __forceinline__ float state_scale(const float (&x)[8], float& inv) {
 
 template <int N, bool G_BF16, bool BITS8>
 __global__ __launch_bounds__(kAdamThreads) void k_adamw(const AdamTable<N> t, const AdamStep a) {
-  // finds a chunk's tensor: lane i holds the first chunk of tensor i
+  // finds a chunk's tensor: lane i holds the first chunk of tensor i (an empty
+  // tensor has that of the one behind it, which is found)
   const int lane = threadIdx.x & 63;
   const int first = lane < t.n ? t.cum[lane < N ? lane : 0] : 0x7FFFFFFF;
   const int chunks = t.cum[t.n];
@@ -146,7 +147,8 @@ __global__ __launch_bounds__(kAdamThreads) void k_adamw(const AdamTable<N> t, co
     const int i = __popcll(__ballot(first <= c)) - 1;
     const int64_t lo = (int64_t)(c - t.cum[i]) * kAdamChunk;
     const int len = c + 1 < t.cum[i + 1] ? kAdamChunk : (int)t.last[i];
-    const uint32_t key = t.key[i] + (uint32_t)((uint64_t)lo >> 32) * 0x27D4EB2Fu;
+    const uint32_t key = mix(mix(a.seed_lo + 0x9E3779B1u * (a.place + (uint32_t)i)) + a.seed_hi) +
+                         (uint32_t)((uint64_t)lo >> 32) * 0x27D4EB2Fu;
     for (int step = 0; step < len; step += kAdamStep) {
       const int at = step + at0;
       if (step + ((int)threadIdx.x >> 4) * 128 >= len) break;  // a group's 16 lanes stay together
@@ -234,7 +236,6 @@ hipError_t adamw(const AdamBatch& b, const AdamStep& a, bool g_bf16, bool bits8,
     t.v_scale[i] = b.v_scale[i];
     t.copy[i] = b.copy[i];
     t.cum[i] = b.cum[i];
-    t.key[i] = b.key[i];
     t.last[i] = b.last[i];
   }
   t.cum[b.n] = b.cum[b.n];

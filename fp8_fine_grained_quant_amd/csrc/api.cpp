@@ -1049,12 +1049,6 @@ fp8q_status fp8q_rms_norm_bwd(const void* dy, const void* x, fp8q_dtype t, int64
 // ------------------------------------------------------------------ AdamW
 namespace {
 
-uint32_t mix32(uint32_t x) {
-  x = (x ^ (x >> 16)) * 0x6C8E9CF5u;
-  x = (x ^ (x >> 15)) * 0xB2D05E13u;
-  return x ^ (x >> 16);
-}
-
 // Whether two of the tensors' parameters share memory (a tensor given twice).
 bool params_overlap(const fp8q_adamw_tensor* t, int64_t n) {
   // ordered as they are as a rule given: one pass; else every pair's order by a sort on the side
@@ -1119,24 +1113,23 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int64_t n, fp8q_dtype g
   a.eps = (float)eps;
   a.norm = norm;
   a.max_norm = max_norm;
-  const uint32_t lo = (uint32_t)seed, hi = (uint32_t)(seed >> 32);
+  a.seed_lo = (uint32_t)seed;
+  a.seed_hi = (uint32_t)(seed >> 32);
   fp8q::AdamBatch b;
   for (int64_t i = 0; i < n;) {
     b.n = 0;
     b.cum[0] = 0;
+    a.place = (uint32_t)i;
     for (; i < n && b.n < fp8q::kMaxAdamTensors; ++i) {
       const fp8q_adamw_tensor& t = tensors[i];
       const int64_t c = cdiv(t.len, fp8q::kAdamChunk);
-      if (c == 0) continue;
       const int k = b.n++;
       b.p[k] = t.p; b.g[k] = t.g; b.m[k] = t.m; b.v[k] = t.v;
       b.m_scale[k] = t.m_scale; b.v_scale[k] = t.v_scale; b.copy[k] = t.copy;
       b.last[k] = (uint16_t)(t.len - (c - 1) * fp8q::kAdamChunk);
       b.cum[k + 1] = b.cum[k] + (int)c;
-      b.key[k] = mix32(mix32(lo + 0x9E3779B1u * (uint32_t)i) + hi);
     }
-    if (b.n == 0) break;
-    if (fp8q::launch_adamw(b, a, gt == FP8Q_BF16, bits == 8, stream) != hipSuccess) return FP8Q_ERR_LAUNCH;
+    if (b.cum[b.n] > 0 && fp8q::launch_adamw(b, a, gt == FP8Q_BF16, bits == 8, stream) != hipSuccess) return FP8Q_ERR_LAUNCH;
   }
   return FP8Q_OK;
 }

@@ -875,26 +875,46 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor* norm = optional(a[14], "norm");
   const double max_norm = real(a[15]);
   const bool codes = lists[kMs].get() != nullptr;
-  const ScalarType state = codes ? at::kByte : at::kFloat;
+  ScalarType state = codes ? at::kByte : at::kFloat;
   ScalarType grad = at::kFloat;
   c10::Device device(c10::kCUDA);
   bool gpu = true;
   const Tensor* abroad = nullptr;
   std::vector<fp8q_adamw_tensor> table((size_t)tensors);
+  // The tensors' objects of a step are seldom in the processor's caches: those of
+  // the next ones are fetched ahead, the Python object first and then the tensor
+  // that it holds (200 tensors of 7 lists: 225 us of host time without).
+  auto ahead = [&](Py_ssize_t i) {
+    for (int l = 0; l < kLists; ++l) {
+      if (!lists[l].get()) continue;
+      if (i + 8 < tensors) __builtin_prefetch(PyTuple_GET_ITEM(lists[l].get(), i + 8));
+      if (i + 4 < tensors) {
+        PyObject* o = PyTuple_GET_ITEM(lists[l].get(), i + 4);
+        if (!THPVariable_Check(o)) continue;
+        const char* impl = reinterpret_cast<const char*>(THPVariable_Unpack(o).unsafeGetTensorImpl());
+        for (size_t at = 0; at < sizeof(c10::TensorImpl); at += 64) __builtin_prefetch(impl + at);
+      }
+    }
+  };
   for (Py_ssize_t i = 0; i < tensors; ++i) {
+    ahead(i);
     const Tensor* t[kLists] = {};
     for (int l = 0; l < kLists; ++l)
       if (lists[l].get()) t[l] = &tensor(PyTuple_GET_ITEM(lists[l].get(), i), names[l]);
     if (i == 0) {
       grad = t[kG]->scalar_type();
       device = t[kP]->device();
+      // codes are bytes; the type that names their format is taken as well
+      if (codes && t[kM]->scalar_type() == at::kFloat8_e4m3fn) state = at::kFloat8_e4m3fn;
     }
     const ScalarType types[kLists] = {at::kFloat, grad, state, state, at::kFloat, at::kFloat, at::kBFloat16};
     const int64_t scales = (t[kP]->numel() + 127) / 128;
     for (int l = 0; l < kLists; ++l) {
       if (!t[l]) continue;
-      if (l == kMs || l == kVs) expect(t[l], {scales}, types[l], names[l]);
-      else expect(t[l], t[kP]->sizes(), types[l], names[l]);
+      const bool scale = l == kMs || l == kVs;
+      if (t[l]->scalar_type() != types[l] ||
+          (scale ? t[l]->dim() != 1 || t[l]->size(0) != scales : t[l]->sizes() != t[kP]->sizes()))
+        expect(t[l], scale ? at::IntArrayRef(scales) : t[kP]->sizes(), types[l], names[l]);  // refuses
       if (!t[l]->is_contiguous()) refuse(PyExc_ValueError, std::string(names[l]) + " must be contiguous");
       gpu = gpu && t[l]->is_cuda();
       if (t[l]->device() != device) abroad = t[l];

@@ -79,6 +79,7 @@ constexpr int kTM = 4, kTN = 8;                   // sub-tiles per wave: 64 x 12
 constexpr int kIA = kBM * kBK / (16 * kNT);       // 16-byte A loads per lane per chunk
 constexpr int kIB = kBN * kBK / (16 * kNT);       // 16-byte B loads per lane per chunk
 constexpr int kMaxChunks = 1024;
+constexpr int kGateUpChunks = 6;                  // chunks left when the gradient's epilogue fetches gate and up
 constexpr int kSkew = 3;                          // promotion trails its MFMA by 3 slots
 static_assert(kTM == 4 && kSkew == kTM - 1, "the slot schedule below assumes 4 row sub-tiles");
 
@@ -512,6 +513,19 @@ __global__ __launch_bounds__(kNT) void k_gemm_fp8(GemmArgs p) {
   };
 
   int c = 0;
+  constexpr bool kGradient = EPI == kEpiDSwiglu;
+  GateUp<kTN> gate_up[kGradient ? kTM : 1];
+  if constexpr (kGradient) {
+    // gate and up of the whole strip, which only the epilogue needs, before the
+    // last chunks (they wait for no value, and the waits below only get stricter)
+    for (; c + 3 <= nk - kGateUpChunks; c += 3) {
+      step(c, IC<0>());
+      step(c + 1, IC<1>());
+      step(c + 2, IC<2>());
+    }
+#pragma unroll
+    for (int i = 0; i < kTM; ++i) gate_up[i].load(po, tc.m0 + w * 64 + 16 * i, tc.mend, tc.n0, lane);
+  }
   for (; c + 3 <= nk; c += 3) {
     step(c, IC<0>());
     step(c + 1, IC<1>());
@@ -534,7 +548,7 @@ __global__ __launch_bounds__(kNT) void k_gemm_fp8(GemmArgs p) {
     store_tile_q<kTM, kTN, 32>(acc, st0 + w * 12288, po, tc.m0 + w * 64, tc.mend, tc.n0, lane);
   } else if constexpr (EPI == kEpiDSwiglu) {
     static_assert(!OUT_F32 && !KG && TR, "gated block's gradient: BF16 Dgrad only");
-    store_tile_dswiglu<kTM, kTN>(acc, st0 + w * 12288, po, tc.m0 + w * 64, tc.mend, tc.n0, lane);
+    store_tile_dswiglu<kTM, kTN, kTM>(acc, st0 + w * 12288, po, tc.m0 + w * 64, tc.mend, tc.n0, lane, gate_up);
   } else {
     store_tile<kTM, kTN, OUT_F32, OUT_F32 ? 16 : 32, 0, TR>(acc, st0 + w * 12288, po, tc.m0 + w * 64, tc.mend, tc.n0,
                                                             lane);
@@ -802,6 +816,11 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
 
   // ---- epilogue: two waves' 12 KB staging areas in each 32 KB region
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  GateUp<kTN> gate_up[2];
+  if constexpr (EPI == kEpiDSwiglu)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      gate_up[i].load(p, tc.m0 + wr * 64 + 16 * i, tc.mend, tc.n0 + wc * 128, lane);
   __builtin_amdgcn_s_barrier();
   fence();
   uint8_t* const ep = (w >> 1) == 0 ? sa0 : (w >> 1) == 1 ? sa1 : (w >> 1) == 2 ? sb0 : sb1;
@@ -818,11 +837,12 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
           up[i][j][r] = acc[i][j + kTN / 2][r];
         }
     // (the block scales in LDS are not needed any more: room for the row maxima)
-    store_tile_swiglu<kTM, 32>(gate, up, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 64, lane, sbk_all,
-                               wr * 64, wc);
+    store_tile_swiglu<kTM>(gate, up, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 64, lane, sbk_all,
+                           wr * 64, wc);
   } else if constexpr (EPI == kEpiDSwiglu) {
     static_assert(!OUT_F32, "gated block's gradient: BF16 Dgrad only");
-    store_tile_dswiglu<kTM, kTN>(acc, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 128, lane);
+    store_tile_dswiglu<kTM, kTN, 2>(acc, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 128, lane,
+                                    gate_up);
   } else if constexpr (EPI == kEpiQuant) {
     static_assert(!OUT_F32 && !GROUPED, "fused output quantization: BF16 Fprop/Dgrad only");
     store_tile_q<kTM, kTN, 32>(acc, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 128, lane);

@@ -73,8 +73,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_swiglu_few(const GemmArgs p,
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int kb = min(k0 + kFewWaves * u, nk - 1);
-      b[u][0] = ld_stream16<1>(B + (int64_t)kb * 128);
-      b[u][1] = ld_stream16<1>(B + (int64_t)kb * 128 + 64);
+      b[u][0] = ld_stream16<0>(B + (int64_t)kb * 128);
+      b[u][1] = ld_stream16<0>(B + (int64_t)kb * 128 + 64);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         a[u][m][0] = ld_stream16<0>(A[m] + (int64_t)kb * 128);
@@ -118,8 +118,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_swiglu_few(const GemmArgs p,
   const int col = n0 + 4 * (at >> 4);
   if (row >= p.M) return;
   auto pack = [](const float4& v) {
-    return make_uint2(f32_to_bf16_rne(v.x) | (f32_to_bf16_rne(v.y) << 16),
-                      f32_to_bf16_rne(v.z) | (f32_to_bf16_rne(v.w) << 16));
+    return make_uint2(pack2_bf16(v.x, v.y), pack2_bf16(v.z, v.w));
   };
   if (p.gu != nullptr) {
     *reinterpret_cast<uint2*>(p.gu + row * p.ld_gu + col) = pack(vg);

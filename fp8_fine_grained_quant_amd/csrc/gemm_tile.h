@@ -3,6 +3,7 @@
 
 #include "device_common.h"
 #include "launch.h"
+#include "row_io.h"
 
 namespace fp8q {
 
@@ -270,10 +271,53 @@ __device__ __forceinline__ void store_tile_q(const float (&acc)[TM][TN][4], uint
 // s = 1 / (1 + exp(-g)).
 
 // By the exponential that cannot overflow, so that s keeps its relative accuracy
-// down to the least numbers (1 / (1 + exp(-g)) is 0 from g = -89 on).
+// down to the least numbers (1 / (1 + exp(-g)) is 0 from g = -89 on):
+// e = exp(-|g|) = (2^-t)^2 with t = |g| log2(e) / 2, whose rounding is made good
+// to first order (the exponential instruction gives no numbers below 2^-126; its
+// square does), and 1 / (1 + e) by the reciprocal instruction.  Each of the two
+// is off by one unit: s by 11 half units in all.  (With the library's expf and
+// an IEEE division the epilogues' arithmetic took twice as long, 81 us against
+// 76 for the gradient of 4096 x 2048 x 7168.)
 __device__ __forceinline__ float sigmoid_f32(float g) {
-  const float e = expf(-fabsf(g));
-  return (g < 0.f ? e : 1.f) / (1.f + e);
+  constexpr float kHalfLog2e = 0.72134752044448170f, kRest = (float)(0.72134752044448170 - (double)kHalfLog2e);
+  constexpr float kLn2 = 0.69314718055994531f;
+  const float a = fmaxf(-fabsf(g), -512.f), t = a * kHalfLog2e;  // e is 0 long before; finite for an infinite g
+  const float lost = __builtin_fmaf(a, kRest, __builtin_fmaf(a, kHalfLog2e, -t));
+  const float h = __builtin_amdgcn_exp2f(t);
+  const float r = __builtin_fmaf(h, lost * kLn2, h), e = r * r;
+  return (g < 0.f ? e : 1.f) * __builtin_amdgcn_rcpf(1.f + e);
+}
+
+// One wave's 16 TM x 16 TN values (layout of store_tile with TRL = 1) as BF16 to
+// a matrix of row stride ld, a full 16-byte row segment at a time.
+template <int TM, int TN>
+__device__ __forceinline__ void store_bf16(const float (&v)[TM][TN][4], uint8_t* ep, uint16_t* out, int64_t ld,
+                                           int64_t row0, int64_t mend, int lane) {
+  constexpr int P = 16 * TN * 2 + 16;            // padded LDS row pitch
+  constexpr int CPR = 2 * TN, RPI = 64 / CPR;    // segments per row, rows per store instruction
+  constexpr int SUB = 12288 / (16 * P) < TM ? 12288 / (16 * P) : TM;  // sub-tiles staged at once
+  static_assert(TM % SUB == 0, "whole passes");
+  const int lg = lane >> 4, l16 = lane & 15;
+#pragma unroll
+  for (int i0 = 0; i0 < TM; i0 += SUB) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the staging area is read out
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = i0; i < i0 + SUB; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        *reinterpret_cast<uint2*>(ep + (16 * (i - i0) + l16) * P + 2 * (16 * j + 4 * lg)) =
+            make_uint2(pack2_bf16(v[i][j][0], v[i][j][1]), pack2_bf16(v[i][j][2], v[i][j][3]));
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int it = 0; it < 16 * SUB / RPI; ++it) {
+      const int rl = it * RPI + lane / CPR, ch = lane % CPR;
+      const int64_t row = row0 + 16 * i0 + rl;
+      const uint4 x = *reinterpret_cast<const uint4*>(ep + rl * P + 16 * ch);
+      if (row < mend) st_stream16<0>(out + row * ld + 8 * ch, x.x, x.y, x.z, x.w);
+    }
+  }
 }
 
 // One wave's gate and up accumulators of the same WM x 64 outputs (layout of
@@ -283,23 +327,14 @@ __device__ __forceinline__ float sigmoid_f32(float g) {
 // two halves are held by two waves, which exchange their rows' max-abs through
 // `half_max` [2][256]: with p.qo every wave of the workgroup makes this call.
 // row_in_tile is the strip's first row in the tile, half the wave's half.
-template <int TM, int ER>
+template <int TM>
 __device__ __forceinline__ void store_tile_swiglu(float (&g)[TM][4][4], const float (&u)[TM][4][4], uint8_t* ep,
                                                   const GemmArgs& p, int64_t row0, int64_t mend, int col0, int lane,
                                                   float* half_max, int row_in_tile, int half) {
   const int lg = lane >> 4, l16 = lane & 15;
-  auto staged = [] {
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the staging area is read out
-    __builtin_amdgcn_wave_barrier();
-  };
-  GemmArgs o = p;
   if (p.gu != nullptr) {
-    o.C = p.gu;
-    o.ldc = p.ld_gu;
-    store_tile<TM, 4, 0, ER, 0, true>(g, ep, o, row0, mend, col0, lane);
-    staged();
-    store_tile<TM, 4, 0, ER, 0, true>(u, ep, o, row0, mend, col0 + (int)p.N, lane);
-    staged();
+    store_bf16<TM, 4>(g, ep, p.gu + col0, p.ld_gu, row0, mend, lane);
+    store_bf16<TM, 4>(u, ep, p.gu + col0 + p.N, p.ld_gu, row0, mend, lane);
   }
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -307,10 +342,7 @@ __device__ __forceinline__ void store_tile_swiglu(float (&g)[TM][4][4], const fl
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) g[i][j][r] = g[i][j][r] * sigmoid_f32(g[i][j][r]) * u[i][j][r];
-  if (p.C != nullptr) {
-    store_tile<TM, 4, 0, ER, 0, true>(g, ep, p, row0, mend, col0, lane);
-    staged();
-  }
+  if (p.C != nullptr) store_bf16<TM, 4>(g, ep, reinterpret_cast<uint16_t*>(p.C) + col0, p.ldc, row0, mend, lane);
   if (p.qo == nullptr) return;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -323,7 +355,7 @@ __device__ __forceinline__ void store_tile_swiglu(float (&g)[TM][4][4], const fl
     m = max(m, (uint32_t)__shfl_xor((int)m, 32));
     if (lg == 0) half_max[half * 256 + row_in_tile + 16 * i + l16] = __uint_as_float(m);
   }
-  __syncthreads();
+  __syncthreads();  // (the staging area is read out as well)
   constexpr int P = 64 + 16;  // padded LDS row pitch of the codes
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -353,92 +385,83 @@ __device__ __forceinline__ void store_tile_swiglu(float (&g)[TM][4][4], const fl
 // u come from p.gu, and
 //   dg = dh u (s + g s (1 - s)),   du = dh g s
 // go to p.C [M, 2N] (BF16, du N columns after dg) and h = g s u to p.h if given.
-// g and u are read, and all outputs written, as full 16-byte row segments
-// through the wave's staging area, one 16-row sub-tile at a time.
-template <int TM, int TN>
+// g and u are read as full 16-byte row segments, a 16-row sub-tile of them a
+// GateUp, AHEAD of them before their use (the narrow tile's kernel loads all
+// before its last chunks, when the memory has little to do).  dh goes through
+// the wave's staging area into the segments' layout, in which the outputs leave
+// from the registers.
+template <int TN>
+struct GateUp {
+  static constexpr int kSegs = 16 * TN * 2 / 16;  // 16-byte segments per row
+  static constexpr int kRows = 64 / kSegs;        // rows per load instruction
+  u32x4 g[16 / kRows], u[16 / kRows];
+
+  __device__ __forceinline__ void load(const GemmArgs& p, int64_t first, int64_t mend, int col0, int lane) {
+#pragma unroll
+    for (int it = 0; it < 16 / kRows; ++it) {
+      // rows past the last one repeat it and are not stored
+      const int64_t row = min(first + it * kRows + lane / kSegs, mend - 1);
+      const uint16_t* src = p.gu + row * p.ld_gu + col0 + 8 * (lane % kSegs);
+      g[it] = ld_stream16<0>(src);
+      u[it] = ld_stream16<0>(src + p.N);
+    }
+  }
+};
+
+template <int TM, int TN, int AHEAD>
 __device__ __forceinline__ void store_tile_dswiglu(const float (&dh)[TM][TN][4], uint8_t* ep, const GemmArgs& p,
-                                                   int64_t row0, int64_t mend, int col0, int lane) {
-  constexpr int WN = 16 * TN;
-  constexpr int P = WN * 2 + 16;        // padded LDS row pitch of 16 rows of BF16
-  constexpr int CPR = WN * 2 / 16;      // 16-byte segments per row
-  constexpr int RPI = 64 / CPR;         // rows per load or store instruction
-  static_assert(2 * 16 * P <= 12288, "two staged sub-tiles fit a wave's staging area");
+                                                   int64_t row0, int64_t mend, int col0, int lane,
+                                                   GateUp<TN> (&held)[AHEAD]) {
+  typedef GateUp<TN> Held;
+  constexpr int P = 16 * TN * 4 + 16;  // padded LDS row pitch of 16 rows of FP32
+  static_assert(16 * P <= 12288, "a sub-tile fits a wave's staging area");
   const int lg = lane >> 4, l16 = lane & 15;
-  uint8_t *const eg = ep, *const eu = ep + 16 * P;
   auto lds_done = [] {
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     __builtin_amdgcn_wave_barrier();
   };
+  uint16_t* const C = reinterpret_cast<uint16_t*>(p.C);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int64_t rfirst = row0 + 16 * i;
-    if (rfirst >= mend) return;
+    const int64_t first = row0 + 16 * i;
     if (i) lds_done();
 #pragma unroll
-    for (int it = 0; it < 16 / RPI; ++it) {
-      const int rl = it * RPI + lane / CPR, ch = lane % CPR;
-      const int64_t row = rfirst + rl;
-      uint4 vg = {0, 0, 0, 0}, vu = {0, 0, 0, 0};
-      if (row < mend) {
-        const uint16_t* src = p.gu + row * p.ld_gu + col0 + 8 * ch;
-        vg = *reinterpret_cast<const uint4*>(src);
-        vu = *reinterpret_cast<const uint4*>(src + p.N);
-      }
-      *reinterpret_cast<uint4*>(eg + rl * P + 16 * ch) = vg;
-      *reinterpret_cast<uint4*>(eu + rl * P + 16 * ch) = vu;
-    }
+    for (int j = 0; j < TN; ++j)
+      *reinterpret_cast<float4*>(ep + l16 * P + 4 * (16 * j + 4 * lg)) =
+          make_float4(dh[i][j][0], dh[i][j][1], dh[i][j][2], dh[i][j][3]);
     lds_done();
-    uint2 hs[TN];
+    Held& gu = held[i % AHEAD];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      uint2* const pg = reinterpret_cast<uint2*>(eg + l16 * P + 2 * (16 * j + 4 * lg));
-      uint2* const pu = reinterpret_cast<uint2*>(eu + l16 * P + 2 * (16 * j + 4 * lg));
-      const uint2 wg = *pg, wu = *pu;
-      float dg[4], du[4], h[4];
+    for (int it = 0; it < 16 / Held::kRows; ++it) {
+      const int rl = it * Held::kRows + lane / Held::kSegs, ch = lane % Held::kSegs;
+      const float4 lo = *reinterpret_cast<const float4*>(ep + rl * P + 32 * ch);
+      const float4 hi = *reinterpret_cast<const float4*>(ep + rl * P + 32 * ch + 16);
+      const float d[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      u32x4 wg, wu, wh;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t bg = r < 2 ? wg.x : wg.y, bu = r < 2 ? wu.x : wu.y;
-        const float g = __uint_as_float(r & 1 ? bg & 0xFFFF0000u : bg << 16);
-        const float u = __uint_as_float(r & 1 ? bu & 0xFFFF0000u : bu << 16);
-        const float s = sigmoid_f32(g), gs = g * s, d = dh[i][j][r];
-        dg[r] = d * u * __builtin_fmaf(gs, 1.f - s, s);
-        du[r] = d * gs;
-        h[r] = gs * u;
+      for (int k = 0; k < 4; ++k) {
+        float dg[2], du[2], h[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float g = __uint_as_float(r ? gu.g[it][k] & 0xFFFF0000u : gu.g[it][k] << 16);
+          const float u = __uint_as_float(r ? gu.u[it][k] & 0xFFFF0000u : gu.u[it][k] << 16);
+          const float s = sigmoid_f32(g), gs = g * s;
+          dg[r] = d[2 * k + r] * u * __builtin_fmaf(gs, 1.f - s, s);
+          du[r] = d[2 * k + r] * gs;
+          h[r] = gs * u;
+        }
+        wg[k] = pack2_bf16(dg[0], dg[1]);
+        wu[k] = pack2_bf16(du[0], du[1]);
+        wh[k] = pack2_bf16(h[0], h[1]);
       }
-      auto pack = [](const float (&v)[4]) {
-        return make_uint2(f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
-                          f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16));
-      };
-      *pg = pack(dg);
-      *pu = pack(du);
-      hs[j] = pack(h);
-    }
-    lds_done();
-    uint16_t* const C = reinterpret_cast<uint16_t*>(p.C);
-#pragma unroll
-    for (int it = 0; it < 16 / RPI; ++it) {
-      const int rl = it * RPI + lane / CPR, ch = lane % CPR;
-      const int64_t row = rfirst + rl;
+      const int64_t row = first + rl;
       if (row >= mend) continue;
-      const uint4 vg = *reinterpret_cast<const uint4*>(eg + rl * P + 16 * ch);
-      const uint4 vu = *reinterpret_cast<const uint4*>(eu + rl * P + 16 * ch);
       uint16_t* dst = C + row * p.ldc + col0 + 8 * ch;
-      st_stream16<0>(dst, vg.x, vg.y, vg.z, vg.w);
-      st_stream16<0>(dst + p.N, vu.x, vu.y, vu.z, vu.w);
+      st_stream16<0>(dst, wg[0], wg[1], wg[2], wg[3]);
+      st_stream16<0>(dst + p.N, wu[0], wu[1], wu[2], wu[3]);
+      if (p.h != nullptr) st_stream16<0>(p.h + row * p.ld_h + col0 + 8 * ch, wh[0], wh[1], wh[2], wh[3]);
     }
-    if (p.h == nullptr) continue;
-    lds_done();
-#pragma unroll
-    for (int j = 0; j < TN; ++j) *reinterpret_cast<uint2*>(eg + l16 * P + 2 * (16 * j + 4 * lg)) = hs[j];
-    lds_done();
-#pragma unroll
-    for (int it = 0; it < 16 / RPI; ++it) {
-      const int rl = it * RPI + lane / CPR, ch = lane % CPR;
-      const int64_t row = rfirst + rl;
-      if (row >= mend) continue;
-      const uint4 v = *reinterpret_cast<const uint4*>(eg + rl * P + 16 * ch);
-      st_stream16<0>(p.h + row * p.ld_h + col0 + 8 * ch, v.x, v.y, v.z, v.w);
-    }
+    if (i + AHEAD < TM) gu.load(p, first + 16 * AHEAD, mend, col0, lane);
   }
 }
 

@@ -241,8 +241,9 @@ hipError_t launch_rms_norm_bwd(const NormRows& a, const void* dy, int64_t ld_dy,
                                hipStream_t st);
 
 // ---------------------------------------------------------------- AdamW
-constexpr int kMaxAdamTensors = 48;  // per launch: the table travels in the kernel's arguments
+constexpr int kMaxAdamTensors = 60;  // per launch: the table travels in the kernel's arguments, 4 KB at most
 constexpr int kAdamChunk = 8192;     // elements of one tensor a block takes at a time
+// Consecutive tensors of a call; empty ones among them have no chunk.
 template <int N>
 struct AdamTable {
   float* p[N];
@@ -253,7 +254,6 @@ struct AdamTable {
   float* v_scale[N];
   uint16_t* copy[N];
   int cum[N + 1];    // first chunk of each tensor, then their number
-  uint32_t key[N];   // of its random numbers
   uint16_t last[N];  // elements of a tensor's last chunk
   uint16_t n;
 };
@@ -264,6 +264,8 @@ struct AdamStep {
   float step;                        // lr / (1 - beta1^t)
   float root;                        // 1 / sqrt(1 - beta2^t)
   float eps;
+  uint32_t seed_lo, seed_hi;         // of the random numbers, with
+  uint32_t place;                    // the place of the table's first tensor in the call's list
   const float* norm;                 // of all gradients, or NULL
   double max_norm;
 };

@@ -100,20 +100,19 @@ __device__ __forceinline__ void store_quantized(const float (&y)[8], uint8_t* q,
   if ((piece & 15) == 0 && (piece >> 4) * 128 < cols) s[piece >> 4] = sc;
 }
 
-// Sum over the block, the same bits in every thread.  `red` holds a value of
-// each wave; the caller alternates between two of them, so that one barrier a
-// call is enough.
-__device__ __forceinline__ float norm_block_sum(float v, float* red) {
+// Sum over a row's threads, `waves` waves from wave `first` of the block on, the
+// same bits in every thread.  `red` holds a value of each wave; the caller
+// alternates between two of them, so that one barrier a call is enough.
+__device__ __forceinline__ float norm_row_sum(float v, float* red, int first, int waves) {
   v = row16_sum(v);
   v += __shfl_xor(v, 16);
   v += __shfl_xor(v, 32);
-  const int waves = (int)blockDim.x >> 6;
   if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  // lane l of every 16 holds wave l's value
+  // lane l of every 16 holds the row's wave l's value
   const int l = threadIdx.x & 15;
-  return row16_sum(l < waves ? red[l] : 0.f);
+  return row16_sum(l < waves ? red[first + l] : 0.f);
 }
 
 template <class Row, int V, bool TINY>
@@ -161,7 +160,7 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
     }
-    ss = norm_block_sum(ss, red[turn]);
+    ss = norm_row_sum(ss, red[turn], 0, (int)blockDim.x >> 6);
     const float rstd = 1.f / sqrtf(__builtin_fmaf(ss, inv_cols, eps));
     if (threadIdx.x == 0) rstd_out[r] = rstd;
 #pragma unroll
@@ -177,22 +176,30 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a
   }
 }
 
+// A block works on as many rows at once as its threads hold (row_threads each):
+// few columns leave a row with few threads, and a block's part of dw is written
+// once however many rows the block has.
 template <class Row, int V, bool TINY>
 __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRows a, const void* dy_, int64_t ld_dy,
                                                                      const void* x_, int64_t ld_x, const float* rstd_in,
                                                                      const void* dsum_, int64_t ld_dsum,
-                                                                     float* __restrict__ part) {
+                                                                     float* __restrict__ part, int row_threads) {
   typedef typename Row::elem elem;
   __shared__ float red[2][16];
+  __shared__ float held[V == 1 ? 8 : 1][V == 1 ? kNormThreads1 : 1];  // dw of the block's rows
   const elem *dy = (const elem*)dy_, *x = (const elem*)x_, *dsum = (const elem*)dsum_;
   elem* dx = (elem*)a.out;
   const int cols = (int)a.cols;
+  // the block's rows and this thread's place among them (a row's threads are whole waves)
+  const int rows_at_once = V == 1 ? (int)blockDim.x / row_threads : 1;
+  const int mine = V == 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / row_threads) : 0;
+  const int t = (int)threadIdx.x - mine * row_threads;
   int piece[V], c0[V];
   bool whole[V];
   float w[V][8], dw[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    piece[i] = i * (int)blockDim.x + (int)threadIdx.x;
+    piece[i] = i * row_threads + t;
     c0[i] = norm_col<Row>(piece[i]);
     whole[i] = no_cut<Row>(c0[i], cols, cols);
     if (V <= kHeldPieces) load_weights<Row>(a.w, c0[i], cols, w[i]);
@@ -201,7 +208,11 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRo
   }
   const float inv_cols = 1.f / (float)cols;
   int turn = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+  for (int64_t r0 = (int64_t)blockIdx.x * rows_at_once; r0 < a.rows;
+       r0 += (int64_t)gridDim.x * rows_at_once, turn ^= 1) {
+    // rows past the last one repeat it and leave nothing
+    const bool on = r0 + mine < a.rows;
+    const int64_t r = on ? r0 + mine : a.rows - 1;
     typename Row::Raw rx[V], rd[V], ro[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -221,12 +232,13 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRo
       if (V > kHeldPieces) load_weights<Row>(again(a.w), c0[i], cols, w[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float t = vd[e] * (vx[e] * rstd);
-        dw[i][e] += t;
-        c = __builtin_fmaf(t, w[i][e], c);
+        const float p = vd[e] * (vx[e] * rstd);
+        if (on) dw[i][e] += p;
+        c = __builtin_fmaf(p, w[i][e], c);
       }
     }
-    c = norm_block_sum(c, red[turn]) * inv_cols;
+    c = norm_row_sum(c, red[turn], mine * (row_threads >> 6), row_threads >> 6) * inv_cols;
+    if (!on) continue;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float vx[8], vd[8], vo[8];
@@ -242,6 +254,15 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRo
       if (dx) store_row_piece<Row, 0>(dx + r * a.ld_out, c0[i], cols, whole[i], Row::pack(vd));
       if (a.q) store_quantized<Row>(vd, a.q + r * a.ld_q, a.s + r * a.ld_s, piece[i], c0[i], cols, whole[i]);
     }
+  }
+  if (V == 1 && rows_at_once > 1) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) held[e][threadIdx.x] = dw[0][e];
+    __syncthreads();
+    if (mine > 0) return;
+    for (int k = 1; k < rows_at_once; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[0][e] += held[e][k * row_threads + t];
   }
   part += (int64_t)blockIdx.x * cols;
 #pragma unroll
@@ -260,40 +281,54 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRo
     }
 }
 
-// dw[c] = the sum of the blocks' parts, 64 columns and 16 runs of parts a block.
-constexpr int kPartCols = 64, kPartRuns = 16;
+// dw[c] = the sum of the blocks' parts: 32 columns and 32 runs of parts a block,
+// several of a run's loads in flight.
+constexpr int kPartCols = 32, kPartRuns = 32, kPartLoads = 8;
 __global__ __launch_bounds__(kPartCols* kPartRuns) void k_norm_parts(const float* __restrict__ part, int parts,
                                                                      int cols, float* __restrict__ dw) {
-  __shared__ float red[kPartRuns][kPartCols];
-  const int c = (int)blockIdx.x * kPartCols + (int)(threadIdx.x & (kPartCols - 1)), run = (int)threadIdx.x / kPartCols;
+  __shared__ float red[kPartRuns][kPartCols + 1];
+  const int lc = (int)(threadIdx.x & (kPartCols - 1)), run = (int)threadIdx.x / kPartCols;
+  const int c = (int)blockIdx.x * kPartCols + lc;
   float s = 0.f;
-  if (c < cols)
-    for (int p = run; p < parts; p += kPartRuns) s += part[(int64_t)p * cols + c];
-  red[run][threadIdx.x & (kPartCols - 1)] = s;
-  __syncthreads();
-  if (run == 0 && c < cols) {
+  if (c < cols) {
+    int p = run;
+    for (; p + (kPartLoads - 1) * kPartRuns < parts; p += kPartLoads * kPartRuns) {
+      float v[kPartLoads];
 #pragma unroll
-    for (int i = 1; i < kPartRuns; ++i) s += red[i][threadIdx.x & (kPartCols - 1)];
-    dw[c] = s;
+      for (int i = 0; i < kPartLoads; ++i) v[i] = part[(int64_t)(p + i * kPartRuns) * cols + c];
+#pragma unroll
+      for (int i = 0; i < kPartLoads; ++i) s += v[i];
+    }
+    for (; p < parts; p += kPartRuns) s += part[(int64_t)p * cols + c];
   }
+  red[run][lc] = s;
+  __syncthreads();
+  // the transposed sums: 32 lanes hold a column's runs
+  s = red[lc][run];
+  s = row16_sum(s);
+  s += __shfl_xor(s, 16);
+  const int col = (int)blockIdx.x * kPartCols + run;
+  if (lc == 0 && col < cols) dw[col] = s;
 }
 
 struct NormShape {
   int v, threads;
 };
-// Pieces of 8 columns, 16 to a group of 128.
+// Pieces of 8 columns, 16 to a group of 128; as many threads as there are, up to
+// the block's most.
 NormShape norm_shape(int64_t cols) {
   const int64_t pieces = (cols + 127) / 128 * 16;
   NormShape n;
-  n.v = pieces <= kNormThreads ? 1 : pieces <= 2 * kNormThreads ? 2 : 4;
+  n.v = pieces <= kNormThreads1 ? 1 : 4;
   n.threads = (int)((pieces + 64 * n.v - 1) / (64 * n.v) * 64);
   return n;
 }
 
-// Blocks that fit the device at once (8 waves a SIMD are not reached at these
-// register counts; 2048 threads a compute unit keep enough loads in flight).
-int64_t norm_blocks(int64_t rows, int threads, int per_cu_threads) {
-  const int64_t most = (int64_t)device_cu_count() * (per_cu_threads / threads < 1 ? 1 : per_cu_threads / threads);
+// Blocks of a launch: as many as the device holds at once, of `waves` waves a
+// compute unit.
+int64_t norm_blocks(int64_t rows, int threads, int waves) {
+  const int per_cu = 64 * waves / threads;
+  const int64_t most = (int64_t)device_cu_count() * (per_cu < 1 ? 1 : per_cu);
   return rows < most ? rows : most;
 }
 
@@ -305,7 +340,6 @@ hipError_t norm_dispatch(bool bf16, int64_t cols, int v, F fn) {
     if (cols < Row::kLen) return fn(row, std::integral_constant<int, 1>{}, std::true_type{});
     switch (v) {
       case 1: return fn(row, std::integral_constant<int, 1>{}, std::false_type{});
-      case 2: return fn(row, std::integral_constant<int, 2>{}, std::false_type{});
       default: return fn(row, std::integral_constant<int, 4>{}, std::false_type{});
     }
   };
@@ -319,7 +353,7 @@ static_assert(4 * kNormThreads * 8 == kMaxNormCols, "the longest row");
 hipError_t launch_rms_norm(const NormRows& a, const void* x, int64_t ld_x, const void* res, int64_t ld_res, float eps,
                            void* sum, int64_t ld_sum, float* rstd, hipStream_t st) {
   const NormShape n = norm_shape(a.cols);
-  const int64_t blocks = norm_blocks(a.rows, n.threads, 2048);
+  const int64_t blocks = norm_blocks(a.rows, n.threads, 32);
   return norm_dispatch(a.bf16, a.cols, n.v, [&](auto row, auto v, auto tiny) {
     hipLaunchKernelGGL((k_rms_norm<decltype(row), decltype(v)::value, decltype(tiny)::value>), dim3((uint32_t)blocks),
                        dim3(n.threads), 0, st, a, x, ld_x, res, ld_res, eps, sum, ld_sum, rstd);
@@ -327,7 +361,16 @@ hipError_t launch_rms_norm(const NormRows& a, const void* x, int64_t ld_x, const
   });
 }
 
-int64_t rms_norm_parts(int64_t rows, int64_t cols) { return norm_blocks(rows, norm_shape(cols).threads, 1024); }
+// Rows that a block of the gradient works on at once.
+static int norm_rows_at_once(const NormShape& n) { return n.v == 1 ? kNormThreads1 / n.threads : 1; }
+
+// One part for each block that runs at once (the registers leave room for 20 waves
+// a compute unit).
+int64_t rms_norm_parts(int64_t rows, int64_t cols) {
+  const NormShape n = norm_shape(cols);
+  const int at_once = norm_rows_at_once(n);
+  return norm_blocks((rows + at_once - 1) / at_once, n.threads * at_once, 20);
+}
 
 hipError_t launch_rms_norm_bwd(const NormRows& a, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
                                const float* rstd, const void* dsum, int64_t ld_dsum, float* part, float* dw,
@@ -337,8 +380,8 @@ hipError_t launch_rms_norm_bwd(const NormRows& a, const void* dy, int64_t ld_dy,
   if (parts > 0) {
     const hipError_t err = norm_dispatch(a.bf16, a.cols, n.v, [&](auto row, auto v, auto tiny) {
       hipLaunchKernelGGL((k_rms_norm_bwd<decltype(row), decltype(v)::value, decltype(tiny)::value>),
-                         dim3((uint32_t)parts), dim3(n.threads), 0, st, a, dy, ld_dy, x, ld_x, rstd, dsum, ld_dsum,
-                         part);
+                         dim3((uint32_t)parts), dim3(n.threads * norm_rows_at_once(n)), 0, st, a, dy, ld_dy, x, ld_x,
+                         rstd, dsum, ld_dsum, part, n.threads);
       return hipGetLastError();
     });
     if (err != hipSuccess) return err;

@@ -213,6 +213,17 @@ def test_shapes_and_tables(bits):
         assert torch.equal(f, p[i].view(-1))
 
 
+def test_codes_of_either_type():
+    """States as bytes or as the type that names their format: the same step."""
+    a, b = Case([700, 31], 8, seed=3), Case([700, 31], 8, seed=3)
+    a.run()
+    as_values = lambda ts: [t.view(torch.float8_e4m3fn) for t in ts]  # noqa: E731
+    fq.adamw(b.p, b.g, as_values(b.m), as_values(b.v), 5, scales=b.scales, seed=77, copies=b.copies, **HYPER)
+    assert all(torch.equal(x, y) for x, y in zip(a.p + a.m + a.v, b.p + b.m + b.v))
+    with pytest.raises(TypeError):
+        fq.adamw(b.p, b.g, as_values(b.m), b.v, 5, 1e-3, scales=b.scales)
+
+
 def test_no_tensors_and_parameters_given_twice():
     fq.adamw([], [], [], [], 1, 1e-3)
     x = [torch.zeros(100, device=DEV)]
