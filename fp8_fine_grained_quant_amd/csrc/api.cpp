@@ -1074,6 +1074,15 @@ bool params_overlap(const fp8q_adamw_tensor* t, int64_t n) {
   return false;
 }
 
+// Elements that a block takes at a time: one step of it while that gives no more
+// blocks than run at once, so that a few small tensors are worked on side by side
+// (60 tensors up to 100000 elements: 10 us with 4 steps a block).
+int adamw_chunk(const fp8q_adamw_tensor* t, int64_t n) {
+  int64_t blocks = 0;
+  for (int64_t i = 0; i < n; ++i) blocks += cdiv(t[i].len, fp8q::kAdamStep);
+  return blocks <= 8 * fp8q::device_cu_count() ? fp8q::kAdamStep : fp8q::kAdamChunk;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1120,13 +1129,15 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int64_t n, fp8q_dtype g
     b.n = 0;
     b.cum[0] = 0;
     a.place = (uint32_t)i;
-    for (; i < n && b.n < fp8q::kMaxAdamTensors; ++i) {
+    const int64_t end = n - i < fp8q::kMaxAdamTensors ? n : i + fp8q::kMaxAdamTensors;
+    a.chunk = adamw_chunk(tensors + i, end - i);
+    for (; i < end; ++i) {
       const fp8q_adamw_tensor& t = tensors[i];
-      const int64_t c = cdiv(t.len, fp8q::kAdamChunk);
+      const int64_t c = cdiv(t.len, a.chunk);
       const int k = b.n++;
       b.p[k] = t.p; b.g[k] = t.g; b.m[k] = t.m; b.v[k] = t.v;
       b.m_scale[k] = t.m_scale; b.v_scale[k] = t.v_scale; b.copy[k] = t.copy;
-      b.last[k] = (uint16_t)(t.len - (c - 1) * fp8q::kAdamChunk);
+      b.last[k] = (uint16_t)(t.len - (c - 1) * a.chunk);
       b.cum[k + 1] = b.cum[k] + (int)c;
     }
     if (b.cum[b.n] > 0 && fp8q::launch_adamw(b, a, gt == FP8Q_BF16, bits == 8, stream) != hipSuccess) return FP8Q_ERR_LAUNCH;

@@ -115,7 +115,8 @@ __device__ __forceinline__ float norm_row_sum(float v, float* red, int first, in
   return row16_sum(l < waves ? red[first + l] : 0.f);
 }
 
-template <class Row, int V, bool TINY>
+// NT: rows come and go past the caches (see past_caches).
+template <class Row, int V, bool TINY, int NT>
 __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a, const void* x_, int64_t ld_x,
                                                                  const void* res_, int64_t ld_res, float eps,
                                                                  void* sum_, int64_t ld_sum, float* rstd_out) {
@@ -139,10 +140,10 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
     typename Row::Raw raw[V], other[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) raw[i] = load_row_piece<Row, TINY, 0>(x + r * ld_x, c0[i], cols, whole[i]);
+    for (int i = 0; i < V; ++i) raw[i] = load_row_piece<Row, TINY, NT>(x + r * ld_x, c0[i], cols, whole[i]);
     if (res)
 #pragma unroll
-      for (int i = 0; i < V; ++i) other[i] = load_row_piece<Row, TINY, 0>(res + r * ld_res, c0[i], cols, whole[i]);
+      for (int i = 0; i < V; ++i) other[i] = load_row_piece<Row, TINY, NT>(res + r * ld_res, c0[i], cols, whole[i]);
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a
         for (int e = 0; e < 8; ++e) v[e] += o[e];
         raw[i] = Row::pack(v);
         Row::unpack(raw[i], v);
-        store_row_piece<Row, 0>(sum + r * ld_sum, c0[i], cols, whole[i], raw[i]);
+        store_row_piece<Row, NT>(sum + r * ld_sum, c0[i], cols, whole[i], raw[i]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
@@ -170,7 +171,7 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a
       if (V > kHeldPieces) load_weights<Row>(again(a.w), c0[i], cols, w[i]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = v[e] * rstd * w[i][e];
-      if (y) store_row_piece<Row, 0>(y + r * a.ld_out, c0[i], cols, whole[i], Row::pack(v));
+      if (y) store_row_piece<Row, NT>(y + r * a.ld_out, c0[i], cols, whole[i], Row::pack(v));
       if (a.q) store_quantized<Row>(v, a.q + r * a.ld_q, a.s + r * a.ld_s, piece[i], c0[i], cols, whole[i]);
     }
   }
@@ -179,7 +180,7 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a
 // A block works on as many rows at once as its threads hold (row_threads each):
 // few columns leave a row with few threads, and a block's part of dw is written
 // once however many rows the block has.
-template <class Row, int V, bool TINY>
+template <class Row, int V, bool TINY, int NT>
 __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRows a, const void* dy_, int64_t ld_dy,
                                                                      const void* x_, int64_t ld_x, const float* rstd_in,
                                                                      const void* dsum_, int64_t ld_dsum,
@@ -216,12 +217,12 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRo
     typename Row::Raw rx[V], rd[V], ro[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      rx[i] = load_row_piece<Row, TINY, 0>(x + r * ld_x, c0[i], cols, whole[i]);
-      rd[i] = load_row_piece<Row, TINY, 0>(dy + r * ld_dy, c0[i], cols, whole[i]);
+      rx[i] = load_row_piece<Row, TINY, NT>(x + r * ld_x, c0[i], cols, whole[i]);
+      rd[i] = load_row_piece<Row, TINY, NT>(dy + r * ld_dy, c0[i], cols, whole[i]);
     }
     if (dsum)
 #pragma unroll
-      for (int i = 0; i < V; ++i) ro[i] = load_row_piece<Row, TINY, 0>(dsum + r * ld_dsum, c0[i], cols, whole[i]);
+      for (int i = 0; i < V; ++i) ro[i] = load_row_piece<Row, TINY, NT>(dsum + r * ld_dsum, c0[i], cols, whole[i]);
     const float rstd = rstd_in[r];
     float c = 0.f;
 #pragma unroll
@@ -251,7 +252,7 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRo
         const float g = __builtin_fmaf(vx[e] * rstd, -c, vd[e] * w[i][e]) * rstd;
         vd[e] = dsum ? g + vo[e] : g;
       }
-      if (dx) store_row_piece<Row, 0>(dx + r * a.ld_out, c0[i], cols, whole[i], Row::pack(vd));
+      if (dx) store_row_piece<Row, NT>(dx + r * a.ld_out, c0[i], cols, whole[i], Row::pack(vd));
       if (a.q) store_quantized<Row>(vd, a.q + r * a.ld_q, a.s + r * a.ld_s, piece[i], c0[i], cols, whole[i]);
     }
   }
@@ -332,18 +333,26 @@ int64_t norm_blocks(int64_t rows, int threads, int waves) {
   return rows < most ? rows : most;
 }
 
-// fn(Row type, pieces per thread, a row may be shorter than a lane's run)
+// Whether `matrices` matrices of the rows' size are too much for the caches (256
+// MB, and what follows finds its rows there if they fit): past them, the norm of
+// 16384 rows of 7168 with residual and codes takes 158 us (166 through them) and
+// its gradient 195 (205); with 4096 rows it is 51 (49), with 2048 29 (24).
+bool past_caches(const NormRows& a, int matrices) {
+  return a.rows * a.cols * (a.bf16 ? 2 : 4) * matrices > ((int64_t)512 << 20);
+}
+
+// fn(Row type, pieces per thread, a row may be shorter than a lane's run, past the caches)
 template <class F>
-hipError_t norm_dispatch(bool bf16, int64_t cols, int v, F fn) {
+hipError_t norm_dispatch(const NormRows& a, int v, bool past, F fn) {
   auto with = [&](auto row) {
     typedef decltype(row) Row;
-    if (cols < Row::kLen) return fn(row, std::integral_constant<int, 1>{}, std::true_type{});
-    switch (v) {
-      case 1: return fn(row, std::integral_constant<int, 1>{}, std::false_type{});
-      default: return fn(row, std::integral_constant<int, 4>{}, std::false_type{});
-    }
+    typedef std::integral_constant<int, 0> Zero;
+    typedef std::integral_constant<int, 1> One;
+    if (a.cols < Row::kLen) return fn(row, One{}, std::true_type{}, Zero{});
+    if (v == 1) return past ? fn(row, One{}, std::false_type{}, One{}) : fn(row, One{}, std::false_type{}, Zero{});
+    return fn(row, std::integral_constant<int, 4>{}, std::false_type{}, Zero{});
   };
-  return bf16 ? with(RowBF16{}) : with(RowF32{});
+  return a.bf16 ? with(RowBF16{}) : with(RowF32{});
 }
 
 }  // namespace
@@ -354,9 +363,10 @@ hipError_t launch_rms_norm(const NormRows& a, const void* x, int64_t ld_x, const
                            void* sum, int64_t ld_sum, float* rstd, hipStream_t st) {
   const NormShape n = norm_shape(a.cols);
   const int64_t blocks = norm_blocks(a.rows, n.threads, 32);
-  return norm_dispatch(a.bf16, a.cols, n.v, [&](auto row, auto v, auto tiny) {
-    hipLaunchKernelGGL((k_rms_norm<decltype(row), decltype(v)::value, decltype(tiny)::value>), dim3((uint32_t)blocks),
-                       dim3(n.threads), 0, st, a, x, ld_x, res, ld_res, eps, sum, ld_sum, rstd);
+  const bool past = past_caches(a, 1 + (res ? 2 : 0) + (a.out ? 1 : 0));
+  return norm_dispatch(a, n.v, past, [&](auto row, auto v, auto tiny, auto nt) {
+    hipLaunchKernelGGL((k_rms_norm<decltype(row), decltype(v)::value, decltype(tiny)::value, decltype(nt)::value>),
+                       dim3((uint32_t)blocks), dim3(n.threads), 0, st, a, x, ld_x, res, ld_res, eps, sum, ld_sum, rstd);
     return hipGetLastError();
   });
 }
@@ -378,8 +388,9 @@ hipError_t launch_rms_norm_bwd(const NormRows& a, const void* dy, int64_t ld_dy,
   const NormShape n = norm_shape(a.cols);
   const int64_t parts = rms_norm_parts(a.rows, a.cols);
   if (parts > 0) {
-    const hipError_t err = norm_dispatch(a.bf16, a.cols, n.v, [&](auto row, auto v, auto tiny) {
-      hipLaunchKernelGGL((k_rms_norm_bwd<decltype(row), decltype(v)::value, decltype(tiny)::value>),
+    const bool past = past_caches(a, 2 + (dsum ? 1 : 0) + (a.out ? 1 : 0));
+    const hipError_t err = norm_dispatch(a, n.v, past, [&](auto row, auto v, auto tiny, auto nt) {
+      hipLaunchKernelGGL((k_rms_norm_bwd<decltype(row), decltype(v)::value, decltype(tiny)::value, decltype(nt)::value>),
                          dim3((uint32_t)parts), dim3(n.threads * norm_rows_at_once(n)), 0, st, a, dy, ld_dy, x, ld_x,
                          rstd, dsum, ld_dsum, part, n.threads);
       return hipGetLastError();
