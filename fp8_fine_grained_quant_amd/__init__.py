@@ -170,7 +170,7 @@ def _open(path):
                               I32),
         "fp8q_rms_norm_bwd_workspace": ([I64, I64], I64),
         "fp8q_gemm_swiglu": ([P, P, P, P, I64, I64, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P], I32),
-        "fp8q_gemm_swiglu_workspace": ([I64, I64, I32], I64),
+        "fp8q_gemm_swiglu_workspace": ([I64, I64, I64, I32], I64),
         "fp8q_grouped_gemm_swiglu": ([P, P, P, P, P, I64, I64, I64, I64, P, I64, P, I64, P, I64, P, I64, P], I32),
         "fp8q_gemm_dgrad_swiglu": ([P, P, P, P, I64, I64, I64, P, I64, P, I64, P, I64, P], I32),
         "fp8q_grouped_gemm_dgrad_swiglu": ([P, P, P, P, P, I64, I64, I64, I64, P, I64, P, I64, P, I64, P], I32),
@@ -996,16 +996,20 @@ def fp8q_rms_norm_bwd(dy, x, weight, rstd, dweight, workspace, dx=None, q=None, 
     _native().rms_norm_bwd(dy, x, weight, rstd, dsum, dx, q, scale, dweight, workspace, None, stream)
 
 
-def gemm_swiglu_workspace(rows, width, codes):
-    """Bytes of workspace that fp8q_gemm_swiglu needs (codes: q is wanted)."""
-    return load_library().fp8q_gemm_swiglu_workspace(rows, width, int(bool(codes)))
+def gemm_swiglu_workspace(rows, width, inner, codes):
+    """Bytes of workspace that fp8q_gemm_swiglu needs on the current device for
+    x [rows, inner] and a block of `width` (codes: q is wanted)."""
+    n = load_library().fp8q_gemm_swiglu_workspace(rows, width, inner, int(bool(codes)))
+    if n < 0:
+        raise ValueError(f"{rows} rows of {inner}, width {width}: out of range")
+    return n
 
 
 def fp8q_gemm_swiglu(xq, xs, wq, ws, h, gu=None, q=None, scale=None, workspace=None, stream=None):
     """Gated feed-forward block: h [M, N] BF16 (or None) = silu(x Wg^T) (x Wu^T)
     for wq [2N, K], gate rows before up rows; gu [M, 2N] BF16 keeps both
     products, q and scale are h's codes.  workspace: gemm_swiglu_workspace(M, N,
-    q is not None) bytes (uint8), None if 0."""
+    K, q is not None) bytes (uint8), None if 0."""
     _native().gemm_swiglu(xq, xs, wq, ws, None, h, gu, q, scale, workspace, None, stream)
 
 

@@ -837,11 +837,8 @@ fp8q_status fp8q_grad_clip(const fp8q_grad* grads, int64_t n, fp8q_dtype ot, dou
 // ---------------------------------------------------- gated feed-forward block
 namespace {
 
-// A launch's threads are counted in 32 bits: tiles of 512 threads, and the
-// few-row kernel's workgroups of 512 threads and 8 columns.
+// A launch's threads are counted in 32 bits: tiles of 512 threads.
 constexpr int64_t kMaxTiles = ((int64_t(1) << 32) - 1) / 512;
-constexpr int64_t kMaxFewWidth = 8 * kMaxTiles;
-bool few_rows(int64_t M, int64_t N) { return M <= fp8q::kFewRows && N <= kMaxFewWidth; }
 
 // The sizes of the gated block's entry points: outputs of gate and of up each,
 // contraction length, 256-row tiles.
@@ -892,9 +889,9 @@ fp8q_status check_dswiglu(const void* gu, int64_t ld_gu, const void* dgu, int64_
 
 extern "C" {
 
-int64_t fp8q_gemm_swiglu_workspace(int64_t M, int64_t N, int codes) {
-  if (M < 0 || N < 0 || M > kMaxDim || N > kMaxDim / 2) return -1;
-  return codes && few_rows(M, N) ? M * N * (int64_t)sizeof(float) : 0;
+int64_t fp8q_gemm_swiglu_workspace(int64_t M, int64_t N, int64_t K, int codes) {
+  if (check_gated(M, N, K, cdiv(M, 256)) != FP8Q_OK) return -1;
+  return codes && fp8q::swiglu_few(M, N, K) ? M * N * (int64_t)sizeof(float) : 0;
 }
 
 fp8q_status fp8q_gemm_swiglu(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, int64_t M,
@@ -906,8 +903,8 @@ fp8q_status fp8q_gemm_swiglu(const uint8_t* xq, const float* xs, const uint8_t* 
   if (const fp8q_status c = check_swiglu_out(h, ld_h, gu, ld_gu, q, ld_q, scale, ld_s, N); c != FP8Q_OK) return c;
   if (!aligned16(xq) || !aligned16(wq) || !aligned4(xs) || !aligned4(ws)) return FP8Q_ERR_ALIGN;
   const GemmArgs a = swiglu_args(xq, xs, wq, ws, M, N, K, h, ld_h, gu, ld_gu, q, ld_q, scale, ld_s);
-  if (few_rows(M, N)) {
-    const int64_t need = fp8q_gemm_swiglu_workspace(M, N, q != nullptr);
+  if (fp8q::swiglu_few(M, N, K)) {
+    const int64_t need = fp8q_gemm_swiglu_workspace(M, N, K, q != nullptr);
     if (need > 0) {
       if (!workspace) return FP8Q_ERR_NULL;
       if (!aligned16(workspace)) return FP8Q_ERR_ALIGN;

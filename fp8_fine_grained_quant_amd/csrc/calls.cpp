@@ -769,7 +769,7 @@ PyObject* gemm_swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
       q = &given_or(nullptr, own_q, {m, width}, at::kByte, xq);
       scale = &given_or(nullptr, own_scale, {m, groups(width)}, at::kFloat, xq);
     }
-    const int64_t need = offsets ? 0 : block.gemm_swiglu_workspace(m, width, q != nullptr);
+    const int64_t need = offsets ? 0 : block.gemm_swiglu_workspace(m, width, k, q != nullptr);
     if (need < 0) check(FP8Q_ERR_SHAPE, "fp8q_gemm_swiglu");
     if (need) room = &given_or(nullptr, own_room, {need}, at::kByte, xq);
   }

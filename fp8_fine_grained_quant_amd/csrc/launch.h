@@ -116,9 +116,10 @@ hipError_t launch_gemm_fp8(const GemmArgs& a, hipStream_t st);
 // through the matrix instruction over `chunks` chunks (1, 2, 4, 8; 0 = all)
 hipError_t launch_gemm_interval(const GemmArgs& a, int chunks, hipStream_t st);
 
-// The gated block of at most kFewRows rows (a.gated == kSwiglu, dense); hf: room
-// for h in FP32 [M, N], needed where codes are wanted.
-constexpr int kFewRows = 64;
+// The gated block of few rows (a.gated == kSwiglu, dense), for sizes of which
+// swiglu_few is true on the current device; hf: room for h in FP32 [M, N], needed
+// where codes are wanted.
+bool swiglu_few(int64_t M, int64_t N, int64_t K);
 hipError_t launch_swiglu_few(const GemmArgs& a, float* hf, hipStream_t st);
 
 // Microscaling (MXFP8 E4M3) quantizers: one E8M0 scale byte per 32

@@ -701,9 +701,12 @@ int64_t fp8q_rms_norm_bwd_workspace(int64_t rows, int64_t cols);
  *   gu     : [M, 2N] BF16: g and u beside each other, for the gradient, or NULL
  *   q, scale : [M, N] codes and [M, N/128] scales of h as it is in FP32, before
  *            its rounding to BF16, or NULL.  One of h, gu and q at least.
- *   workspace : 16-byte aligned, fp8q_gemm_swiglu_workspace(M, N, q wanted) bytes
- * More than 64 rows have the accuracy of fp8q_gemm_fprop in g and u; up to 64
- * rows run on a kernel for few rows with that of fp8q_gemm_fprop_exact.
+ *   workspace : 16-byte aligned, fp8q_gemm_swiglu_workspace(M, N, K, q wanted) bytes
+ *            on the current device
+ * g and u have the accuracy of fp8q_gemm_fprop.  Where few rows would leave most of
+ * the device without a tile, a kernel for few rows runs, with the accuracy of
+ * fp8q_gemm_fprop_exact (by the sizes and the device's compute units alone: up to
+ * 384 rows of a block of width 2048, up to 16 of any below 20000).
  * Rules: N % 128 == 0, K % 128 == 0, K <= 131072, any M >= 0; xq, wq, h, gu, q
  * 16-byte aligned with row strides that are multiples of 16 bytes.
  */
@@ -712,7 +715,7 @@ fp8q_status fp8q_gemm_swiglu(const uint8_t* xq, const float* xs, const uint8_t* 
                              int64_t ld_q, float* scale, int64_t ld_s, void* workspace, int64_t workspace_bytes,
                              hipStream_t stream);
 /* Bytes of workspace that call needs (-1: sizes out of range). */
-int64_t fp8q_gemm_swiglu_workspace(int64_t M, int64_t N, int codes);
+int64_t fp8q_gemm_swiglu_workspace(int64_t M, int64_t N, int64_t K, int codes);
 
 /*
  * The same by expert: rows [o_e, o_{e+1}) use the expert's own wq [E, 2N, K] and

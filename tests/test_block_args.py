@@ -91,8 +91,8 @@ def test_swiglu(lib, grouped):
         assert f(e=0) == SHAPE and f(e=65537) == SHAPE
         return
     work = lib.fp8q_gemm_swiglu_workspace
-    assert work(64, 256, 1) == 64 * 256 * 4 and work(64, 256, 0) == 0 and work(65, 256, 1) == 0
-    assert work(-1, 256, 1) == -1 and work(4, BIG, 1) == -1
+    assert work(64, 256, 384, 1) == 64 * 256 * 4 and work(64, 256, 384, 0) == 0 and work(8192, 2048, 7168, 1) == 0
+    assert work(-1, 256, 384, 1) == -1 and work(4, BIG, 384, 1) == -1 and work(4, 256, 100, 1) == -1
     assert f(m=64) == NULL and f(m=64, room=A + 4, nroom=1 << 20) == ALIGN and f(m=64, room=A, nroom=65535) == SHAPE
 
 

@@ -12,7 +12,12 @@ from gpu_util import DEV, log
 
 pytestmark = pytest.mark.gpu
 BF16, U8, U = torch.bfloat16, torch.uint8, ref.U
-FEW = 64  # rows up to which the products are exact
+
+
+def few(m, f, k):
+    """Whether the kernel for few rows, whose products are exact, takes these
+    sizes: it is the one that needs room for codes."""
+    return fq.gemm_swiglu_workspace(m, f, k, True) > 0
 
 
 def operands(m, f, k, experts=0, seed=1, std=1.0):
@@ -53,14 +58,15 @@ def check_block(xq, xs, wq, ws, h=None, gu=None, q=None, s=None, exact=False):
 
 DENSE = [(1, 128, 128), (2, 128, 384), (8, 2048, 1024), (15, 256, 640), (16, 384, 7168), (17, 128, 256), (31, 256, 512),
          (33, 640, 896), (48, 128, 1152), (64, 512, 2048), (65, 128, 128), (65, 256, 640), (100, 384, 512),
-         (256, 128, 1024), (257, 256, 384), (300, 640, 1792), (1000, 128, 256), (513, 1024, 2048)]
+         (256, 128, 1024), (257, 256, 384), (300, 640, 1792), (1000, 128, 256), (513, 1024, 2048), (3, 128, 131072 // 8),
+         (40, 128, 9 * 1024), (130, 128, 11 * 1024), (16, 8192, 128), (1300, 2048, 256), (2000, 1024, 896)]
 
 
 @pytest.mark.parametrize("m, f, k", DENSE)
 def test_block(m, f, k):
     ops = operands(m, f, k)
     h, gu, q, s = fq.gemm_swiglu_quant(*ops, with_output=True, with_gu=True)
-    check_block(*ops, h, gu, q, s, exact=m <= FEW)
+    check_block(*ops, h, gu, q, s, exact=few(m, f, k))
     # each output alone is what it is beside the others
     h2, none = fq.gemm_swiglu(*ops)
     assert none is None and torch.equal(h2, h)
@@ -69,6 +75,13 @@ def test_block(m, f, k):
     none, none2, q4, s4 = fq.gemm_swiglu_quant(*ops)
     assert none is None and none2 is None and torch.equal(q4, q) and torch.equal(s4, s)
     log(f"swiglu {m}x{f}x{k}")
+
+
+def test_both_kernels_are_taken():
+    """Few rows of every width go to one, many rows to the other, and the cases
+    above have both on either side."""
+    assert few(1, 128, 128) and few(8, 2048, 7168) and few(64, 2048, 7168) and not few(4096, 2048, 7168)
+    assert {few(*c) for c in DENSE if c[0] > 64} == {few(*c) for c in DENSE if c[0] <= 64} == {True, False}
 
 
 def offsets_of(counts):
@@ -178,15 +191,15 @@ def test_extreme_gates():
     check_gradient(dyq, dys, weight_values(wt, ws, n), gu, dgu, h)
     assert bool(torch.isfinite(dgu).all())
     # and forward, through a weight whose gates are that large
-    for rows in (5, 80):
+    for rows in (5, 3000):
         xq, xs, wq, ws2 = operands(rows, 128, 128, seed=9)
         ws2 = ws2.clone()
         ws2[0] *= 300.0
         h, gu2, q, s = fq.gemm_swiglu_quant(xq, xs, wq, ws2, with_output=True, with_gu=True)
-        check_block(xq, xs, wq, ws2, h, gu2, q, s, exact=rows <= FEW)
+        check_block(xq, xs, wq, ws2, h, gu2, q, s, exact=few(rows, 128, 128))
 
 
-@pytest.mark.parametrize("m", [9, 64, 90])
+@pytest.mark.parametrize("m", [9, 64, 90, 2000])
 def test_strided_outputs_and_rows_behind(m):
     """Outputs within wider rows, more rows behind them: nothing else is written."""
     f, k = 256, 384
@@ -196,7 +209,7 @@ def test_strided_outputs_and_rows_behind(m):
     gu = torch.full((m + 3, 2 * f + 16), 7.0, dtype=BF16, device=DEV)
     q = torch.full((m + 3, f + 16), 99, dtype=U8, device=DEV)
     s = torch.full((m + 3, f // 128 + 1), 7.0, device=DEV)
-    room = torch.empty(fq.gemm_swiglu_workspace(m, f, True), dtype=U8, device=DEV)
+    room = torch.empty(fq.gemm_swiglu_workspace(m, f, k, True), dtype=U8, device=DEV)
     fq.fp8q_gemm_swiglu(*ops, h[:m, :f], gu[:m, :2 * f], q[:m, :f], s[:m, :f // 128], room)
     for got, w, fill in ((h, want[0], 7), (gu, want[1], 7), (q, want[2], 99), (s, want[3], 7)):
         assert torch.equal(got[:m, :w.shape[1]], w)
@@ -218,7 +231,7 @@ def test_no_rows():
     assert h.shape == (0, 128) and gu.shape == (0, 256) and q.shape == (0, 128) and s.shape == (0, 1)
 
 
-@pytest.mark.parametrize("m", [8, 200])
+@pytest.mark.parametrize("m", [8, 200, 3000])
 def test_captured(m):
     """Replays with new inputs written between them, two graphs in turn."""
     f, k = 256, 640
