@@ -1046,29 +1046,49 @@ fp8q_status fp8q_rms_norm_bwd(const void* dy, const void* x, fp8q_dtype t, int64
 // ------------------------------------------------------------------ AdamW
 namespace {
 
-// Whether two of the tensors' parameters share memory (a tensor given twice).
-bool params_overlap(const fp8q_adamw_tensor* t, int64_t n) {
-  // ordered as they are as a rule given: one pass; else every pair's order by a sort on the side
+// Whether two tensors of one list share memory (a tensor given twice); list gives
+// the first byte of tensor i and its bytes.
+template <class F>
+bool list_overlaps(int64_t n, F list) {
+  // tensors that lie in the order of the list, or in the other one, take one pass
   bool rising = true, falling = true;
-  const float *end = nullptr, *begin = nullptr;
+  uintptr_t begin = UINTPTR_MAX, end = 0;
   for (int64_t i = 0; i < n; ++i) {
-    if (t[i].len == 0) continue;
-    if (end) {
-      rising = rising && t[i].p >= end;
-      falling = falling && t[i].p + t[i].len <= begin;
-    }
-    end = t[i].p + t[i].len;
-    begin = t[i].p;
+    const auto [at, bytes] = list(i);
+    if (at == 0 || bytes == 0) continue;
+    rising = rising && at >= end;
+    falling = falling && at + bytes <= begin;
+    begin = at;
+    end = at + bytes;
   }
   if (rising || falling) return false;
-  std::vector<std::pair<const float*, int64_t>> at;
-  at.reserve((size_t)n);
-  for (int64_t i = 0; i < n; ++i)
-    if (t[i].len > 0) at.emplace_back(t[i].p, t[i].len);
-  std::sort(at.begin(), at.end());
-  for (size_t i = 1; i < at.size(); ++i)
-    if (at[i].first < at[i - 1].first + at[i - 1].second) return true;
+  std::vector<std::pair<uintptr_t, uintptr_t>> all;
+  all.reserve((size_t)n);
+  for (int64_t i = 0; i < n; ++i) {
+    const auto [at, bytes] = list(i);
+    if (at != 0 && bytes != 0) all.emplace_back(at, bytes);
+  }
+  std::sort(all.begin(), all.end());
+  for (size_t i = 1; i < all.size(); ++i)
+    if (all[i].first < all[i - 1].first + all[i - 1].second) return true;
   return false;
+}
+
+// Whether a list of what the step writes holds memory twice.
+bool adamw_overlaps(const fp8q_adamw_tensor* t, int64_t n, int bits) {
+  const int64_t state = bits == 8 ? 1 : 4;
+  auto over = [&](auto member, auto bytes) {
+    return list_overlaps(n, [&](int64_t i) {
+      return std::pair<uintptr_t, uintptr_t>(reinterpret_cast<uintptr_t>(t[i].*member), (uintptr_t)bytes(t[i].len));
+    });
+  };
+  if (over(&fp8q_adamw_tensor::p, [](int64_t len) { return 4 * len; }) ||
+      over(&fp8q_adamw_tensor::m, [&](int64_t len) { return state * len; }) ||
+      over(&fp8q_adamw_tensor::v, [&](int64_t len) { return state * len; }) ||
+      over(&fp8q_adamw_tensor::copy, [](int64_t len) { return 2 * len; }))
+    return true;
+  auto scales = [](int64_t len) { return 4 * cdiv(len, 128); };
+  return bits == 8 && (over(&fp8q_adamw_tensor::m_scale, scales) || over(&fp8q_adamw_tensor::v_scale, scales));
 }
 
 // Elements that a block takes at a time: one step of it while that gives no more
@@ -1106,7 +1126,7 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int64_t n, fp8q_dtype g
       return FP8Q_ERR_ALIGN;
   }
   try {
-    if (params_overlap(tensors, n)) return FP8Q_ERR_SHAPE;
+    if (adamw_overlaps(tensors, n, bits)) return FP8Q_ERR_SHAPE;
   } catch (const std::bad_alloc&) {  // no memory for the check
     return FP8Q_ERR_LAUNCH;
   }
@@ -1117,6 +1137,8 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int64_t n, fp8q_dtype g
   a.step = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
   a.root = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
   a.eps = (float)eps;
+  if (!std::isfinite(a.keep) || !std::isfinite(a.step) || !std::isfinite(a.root) || !std::isfinite(a.eps))
+    return FP8Q_ERR_SHAPE;  // numbers that FP32 does not hold
   a.norm = norm;
   a.max_norm = max_norm;
   a.seed_lo = (uint32_t)seed;

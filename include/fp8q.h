@@ -774,8 +774,9 @@ fp8q_status fp8q_grouped_gemm_dgrad_swiglu(const uint8_t* dyq, const float* dys,
  * keeps the roundings independent.  A gradient that is not finite makes its group
  * of 128 states NaN.
  * 0 <= beta < 1, eps >= 0, max_norm >= 0 (inf: no clipping).  Tensors start at any
- * element and must not overlap each other (parameters that do are refused,
- * FP8Q_ERR_SHAPE).  The numbers of the step are read at the call: a captured call
+ * element and must not overlap each other (a list of parameters, states, scales or
+ * copies that holds memory twice is refused, FP8Q_ERR_SHAPE, as are numbers of the
+ * step that FP32 does not hold).  The numbers of the step are read at the call: a captured call
  * repeats the same step.
  */
 typedef struct {

@@ -131,7 +131,7 @@ def adamw_call(lib, tensors, n=None, gt=1, bits=32, lr=1e-3, b1=0.9, b2=0.95, ep
 
 
 def test_adamw(lib):
-    base = dict(p=A, g=A, m=A, v=A, ms=A, vs=A, copy=A, len=100)
+    base = dict(p=A, g=A, m=A, v=A, ms=A, vs=A, copy=A, len=100)  # one tensor: its own parts are not compared
     one = lambda **k: [tuple({**base, **k}.values())]  # noqa: E731
     assert adamw_call(lib, []) == OK and adamw_call(lib, one(len=0, p=None)) == OK
     assert adamw_call(lib, [], n=3) == NULL and adamw_call(lib, [], n=-1) == SHAPE
@@ -139,7 +139,7 @@ def test_adamw(lib):
     nan, inf = float("nan"), float("inf")
     for bad in (dict(bits=16), dict(bits=0), dict(step=0), dict(step=-3), dict(b1=1.0), dict(b1=-0.1), dict(b2=1.0),
                 dict(b2=nan), dict(eps=-1e-8), dict(eps=nan), dict(eps=inf), dict(lr=nan), dict(lr=inf), dict(wd=nan),
-                dict(wd=inf), dict(most=-1.0), dict(most=nan)):
+                dict(wd=inf), dict(lr=1e300), dict(eps=1e39), dict(most=-1.0), dict(most=nan)):
         assert adamw_call(lib, one(), **bad) == SHAPE, bad
     assert adamw_call(lib, one(len=-1)) == SHAPE and adamw_call(lib, one(len=1 << 45)) == SHAPE
     for name in ("p", "g", "m", "v"):
@@ -155,8 +155,17 @@ def test_adamw(lib):
 
 @pytest.mark.parametrize("at", [[0, 0], [0, 396], [4000, 0, 3604], [800, 400, 0, 420], [0, 1200, 2400, 1100]])
 def test_adamw_refuses_parameters_given_twice(lib, at):
-    t = [(A + a, A, A, A, A, A, None, 100) for a in at]
-    assert adamw_call(lib, t) == SHAPE
+    free = lambda i: A + (1 << 16) * (i + 1)  # noqa: E731
+    for which, bits in ((0, 32), (2, 32), (3, 32), (0, 8), (6, 8)):
+        t = [[free(i) + (k << 14) for k in range(7)] + [100] for i in range(len(at))]
+        for i, a in enumerate(at):
+            t[i][which] = A + (a if which != 6 else a // 2)
+        assert adamw_call(lib, [tuple(x) for x in t], bits=bits) == SHAPE, (which, bits)
+    for which in (2, 3):  # codes: 100 bytes a tensor
+        t = [[free(i) + (k << 14) for k in range(7)] + [100] for i in range(len(at))]
+        for i, a in enumerate(at):
+            t[i][which] = A + a // 4
+        assert adamw_call(lib, [tuple(x) for x in t], bits=8) == SHAPE, which
 
 
 def z(*shape, dt=f32):
