@@ -132,7 +132,7 @@ __device__ __forceinline__ float state_scale(const float (&x)[8], float& inv) {
   for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[e]));
   m = max(row16_max_u32(m), __float_as_uint(kAmaxFloor));
   if (m >= 0x7F800000u) m = 0x7FC00000u;
-  inv = kFp8Max / __uint_as_float(m);
+  inv = 1.f / __uint_as_float(m) * kFp8Max;
   return __uint_as_float(m) / kFp8Max;
 }
 
@@ -183,8 +183,11 @@ __global__ __launch_bounds__(kAdamThreads) void k_adamw(const AdamTable<N> t, co
       for (int e = 0; e < 8; ++e) {
         if (BITS8) v[e] *= v[e];
         if (a.norm) g[e] = (float)((double)g[e] * factor);
-        m[e] = __builtin_fmaf(a.beta1, m[e], a.rest1 * g[e]);
-        v[e] = __builtin_fmaf(a.beta2, v[e], a.rest2 * (g[e] * g[e]));
+        // every product and sum rounded on its own: a state in 8 bits goes by the
+        // last bits of its value where that is near a border of the rounding, and
+        // these are the bits that the formula gives, term by term
+        m[e] = a.beta1 * m[e] + a.rest1 * g[e];
+        v[e] = a.beta2 * v[e] + a.rest2 * (g[e] * g[e]);
         const float root = sqrtf(v[e]);
         p[e] = __builtin_fmaf(p[e], a.keep, -(a.step * m[e] / __builtin_fmaf(root, a.root, a.eps)));
         if (BITS8) v[e] = root;

@@ -763,7 +763,7 @@ fp8q_status fp8q_grouped_gemm_dgrad_swiglu(const uint8_t* dyq, const float* dys,
  *             c = 1 if norm <= max_norm, else max_norm / norm, which and whose
  *             product with g are in 64 bits as there; NULL: c = 1
  * bits = 8: the step uses m and v in FP32 and rounds them behind it, scale =
- * fl32(max(amax, 2^-100) / 448), y = x * fl32(448 / max(amax, 2^-100)), to one of
+ * fl32(a / 448), a = max(amax, 2^-100), y = x * fl32(fl32(1 / a) * 448), to one of
  * the two E4M3 values around y: away from zero where floor(t + u) > floor(t), t = |y|
  * in steps of E4M3 there, u in [0, 1) of 16 random bits, the lower ones of the
  * element's 32 for m, the upper ones for sqrt(v).  sqrt(v) > 0 is never rounded to
