@@ -593,7 +593,10 @@ static_assert(4 * kBM * kBK + 4 * 2 * kMaxChunks + 4 * 2 * 256 * 4 + 1024 <= 160
 // wave's strip holds both of its 64 output columns (sub-tiles 0-3 gate, 4-7
 // up), so the activation and the product are formed in registers.  SC4 false
 // (scale rows that are not 16-byte aligned): the row scales come 4 bytes per row
-// and chunk, into a ring of 8 chunks.
+// and chunk, into a ring of 8 chunks.  4096 x 2048 x 7168 with gate and up kept:
+// 101 us, 2.4 PFLOP/s (the same product alone, 4096 x 4096 x 7168: 96 to 101);
+// 16384 rows over 32 experts 495 us (512 where a strip without rows was worked on
+// like the others).
 template <int OUT_F32, bool GROUPED, int EPI, bool SC4 = true>
 __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -610,7 +613,11 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
   if (!tile_coord<kBM, GLU ? kWBN / 2 : kWBN, GROUPED>(p, tc)) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wr = w & 3, wc = w >> 2;  // the wave's 64-row strip and 128-column half (GLU: 64 outputs)
+  // the wave's 64-row strip and 128-column half (GLU: 64 outputs), and its part of
+  // the loads.  GLU gives a strip's two waves to two SIMDs, so that a tile of few
+  // rows keeps all four busy.
+  const int wr = GLU ? w >> 1 : w & 3, wc = GLU ? w & 1 : w >> 2;
+  const int lr = w & 3, lh = w >> 2;
   const int l16 = lane & 15, g = lane >> 4;
   const int nk = (int)(p.K / kBK);
   const uint8_t* Bp = p.B + (GROUPED ? (int64_t)tc.e * p.b_estride : 0);
@@ -620,14 +627,14 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
   // direct-load sources, range-checked as in k_gemm_fp8
   const __amdgpu_buffer_rsrc_t rA = make_rsrc(p.A + tc.m0 * p.lda, (uint32_t)(rows * p.lda));
   // (GLU: waves 0-3 load the gate rows, waves 4-7 the up rows)
-  const int64_t b0 = tc.n0 + (GLU && wc ? p.N : 0);
+  const int64_t b0 = tc.n0 + (GLU && lh ? p.N : 0);
   const __amdgpu_buffer_rsrc_t rB = make_rsrc(Bp + b0 * p.ldb, (uint32_t)((GLU ? kWBN / 2 : kWBN) * p.ldb));
   const __amdgpu_buffer_rsrc_t rSa = make_rsrc(p.sa + tc.m0 * p.ld_sa, (uint32_t)(rows * p.ld_sa * 4));
   const int r8 = lane >> 3, lc = (lane & 7) ^ r8;
   const uint32_t voffA = (uint32_t)((w * kWIA * 8 + r8) * p.lda + 16 * lc);
-  const uint32_t voffB = (uint32_t)(((GLU ? wr : w) * kWIB * 8 + r8) * p.ldb + 16 * lc);
+  const uint32_t voffB = (uint32_t)(((GLU ? lr : w) * kWIB * 8 + r8) * p.ldb + 16 * lc);
   const uint32_t stepA = (uint32_t)(8 * p.lda), stepB = (uint32_t)(8 * p.ldb);
-  const uint32_t voffSa = (uint32_t)(min(wr * 64 + lane, rows - 1) * p.ld_sa * 4);
+  const uint32_t voffSa = (uint32_t)(min(lr * 64 + lane, rows - 1) * p.ld_sa * 4);
 
   // d-th A-side load of chunk kb into A region `ar` (d == kWIA: waves 0-3 load
   // the row scales of the 4-chunk block that starts at kb; every other wave
@@ -717,11 +724,11 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
   // loads as in k_gemm_fp8: waves 0-3 the first half, 4-7 the second); A(0),
   // B(0), A(1), B(1) in flight in that order; chunk 0 published
   {
-    const float* psb = sbp + (GLU ? b0 / 128 : (int64_t)(tc.n0 / 128 + wc)) * p.sb_rs;
+    const float* psb = sbp + (GLU ? b0 / 128 : (int64_t)(tc.n0 / 128 + lh)) * p.sb_rs;
     const __amdgpu_buffer_rsrc_t rK = make_rsrc(psb, (uint32_t)(((int64_t)(nk - 1) * p.sb_cs + 1) * 4));
     for (int r = 0; r * 256 < nk; ++r)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rK, (lds_ptr)(sbk_all + wc * kMaxChunks + r * 256 + wr * 64), 4,
-                                               (uint32_t)((r * 256 + wr * 64 + lane) * p.sb_cs * 4), 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rK, (lds_ptr)(sbk_all + lh * kMaxChunks + r * 256 + lr * 64), 4,
+                                               (uint32_t)((r * 256 + lr * 64 + lane) * p.sb_cs * 4), 0, 0, 0);
   }
   fence();
 #pragma unroll
@@ -806,11 +813,32 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
   };
 
   int c = 0;
-  for (; c + 2 <= nk; c += 2) {
-    step(c, IC<0>());
-    step(c + 1, IC<1>());
+  if (GLU && wr * 64 >= rows) {
+    // a strip without rows (a tile that ends an expert): its part of the loads, at
+    // the other waves' barriers
+    auto idle = [&](int kc, auto U) {
+      constexpr int u = decltype(U)::value;
+      const int c2 = min(kc + 2, nk - 1);
+      __builtin_amdgcn_s_barrier();
+#pragma unroll
+      for (int d = 0; d < kWDmaA; ++d) issue_a(c2, u == 0 ? sa0 : sa1, d);
+      __builtin_amdgcn_s_waitcnt(kWaitA);
+      __builtin_amdgcn_s_barrier();
+#pragma unroll
+      for (int q = 0; q < kWIB; ++q) issue_b(c2, u == 0 ? sb0 : sb1, q);
+    };
+    for (; c + 2 <= nk; c += 2) {
+      idle(c, IC<0>());
+      idle(c + 1, IC<1>());
+    }
+    if (c < nk) idle(c, IC<0>());
+  } else {
+    for (; c + 2 <= nk; c += 2) {
+      step(c, IC<0>());
+      step(c + 1, IC<1>());
+    }
+    if (c < nk) step(c, IC<0>());
   }
-  if (c < nk) step(c, IC<0>());
 #pragma unroll
   for (int i = 1; i < kTM; ++i) promote(i, kTN - 1);
 
