@@ -33,11 +33,9 @@ namespace fp8q {
 
 namespace {
 
-// 8-column pieces per thread (V): 1 up to 8192 columns, else 4, with which the
+// 8-column pieces per thread (V): 1 up to 8192 columns, else 2, with which the
 // weights do not fit in the registers and come anew for every row.
-constexpr int kNormThreads1 = 1024, kNormThreads = 512;
-template <int V>
-constexpr int norm_threads() { return V == 1 ? kNormThreads1 : kNormThreads; }
+constexpr int kNormThreads = 1024;
 
 template <class Row>
 __device__ __forceinline__ int norm_col(int piece) { return (piece >> 4) * 128 + (piece & 15) * Row::kLen; }
@@ -123,7 +121,7 @@ __device__ __forceinline__ float norm_row_sum(float v, float* red, int first, in
 
 // NT: rows come and go past the caches (see past_caches).
 template <class Row, int V, bool TINY, int NT>
-__global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a, const void* x_, int64_t ld_x,
+__global__ __launch_bounds__(kNormThreads) void k_rms_norm(const NormRows a, const void* x_, int64_t ld_x,
                                                                  const void* res_, int64_t ld_res, float eps,
                                                                  void* sum_, int64_t ld_sum, float* rstd_out) {
   typedef typename Row::elem elem;
@@ -187,13 +185,13 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm(const NormRows a
 // few columns leave a row with few threads, and a block's part of dw is written
 // once however many rows the block has.
 template <class Row, int V, bool TINY, int NT>
-__global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRows a, const void* dy_, int64_t ld_dy,
+__global__ __launch_bounds__(kNormThreads) void k_rms_norm_bwd(const NormRows a, const void* dy_, int64_t ld_dy,
                                                                      const void* x_, int64_t ld_x, const float* rstd_in,
                                                                      const void* dsum_, int64_t ld_dsum,
                                                                      float* __restrict__ part, int row_threads) {
   typedef typename Row::elem elem;
   __shared__ float red[2][16];
-  __shared__ float held[V == 1 ? 8 : 1][V == 1 ? kNormThreads1 : 1];  // dw of the block's rows
+  __shared__ float held[V == 1 ? 8 : 1][V == 1 ? kNormThreads : 1];  // dw of the block's rows
   const elem *dy = (const elem*)dy_, *x = (const elem*)x_, *dsum = (const elem*)dsum_;
   elem* dx = (elem*)a.out;
   const int cols = (int)a.cols;
@@ -226,7 +224,9 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRo
       rx[i] = load_row_piece<Row, TINY, NT>(x + r * ld_x, c0[i], cols, whole[i]);
       rd[i] = load_row_piece<Row, TINY, NT>(dy + r * ld_dy, c0[i], cols, whole[i]);
     }
-    if (dsum)
+    // (two pieces of FP32 rows leave no registers for the stream's gradient yet)
+    constexpr bool kLate = V > 1 && Row::kRuns == 2;
+    if (dsum && !kLate)
 #pragma unroll
       for (int i = 0; i < V; ++i) ro[i] = load_row_piece<Row, TINY, NT>(dsum + r * ld_dsum, c0[i], cols, whole[i]);
     const float rstd = rstd_in[r];
@@ -251,6 +251,7 @@ __global__ __launch_bounds__(norm_threads<V>()) void k_rms_norm_bwd(const NormRo
       float vx[8], vd[8], vo[8];
       Row::unpack(rx[i], vx);
       Row::unpack(rd[i], vd);
+      if (dsum && kLate) ro[i] = load_row_piece<Row, TINY, NT>(dsum + r * ld_dsum, c0[i], cols, whole[i]);
       if (dsum) Row::unpack(ro[i], vo);
       if (V > 1) load_weights<Row>(again(a.w), c0[i], cols, w[i]);
 #pragma unroll
@@ -326,7 +327,7 @@ struct NormShape {
 NormShape norm_shape(int64_t cols) {
   const int64_t pieces = (cols + 127) / 128 * 16;
   NormShape n;
-  n.v = pieces <= kNormThreads1 ? 1 : 4;
+  n.v = pieces <= kNormThreads ? 1 : 2;
   n.threads = (int)((pieces + 64 * n.v - 1) / (64 * n.v) * 64);
   return n;
 }
@@ -356,14 +357,14 @@ hipError_t norm_dispatch(const NormRows& a, int v, bool past, F fn) {
     typedef std::integral_constant<int, 1> One;
     if (a.cols < Row::kLen) return fn(row, One{}, std::true_type{}, Zero{});
     if (v == 1) return past ? fn(row, One{}, std::false_type{}, One{}) : fn(row, One{}, std::false_type{}, Zero{});
-    return fn(row, std::integral_constant<int, 4>{}, std::false_type{}, Zero{});
+    return fn(row, std::integral_constant<int, 2>{}, std::false_type{}, Zero{});
   };
   return a.bf16 ? with(RowBF16{}) : with(RowF32{});
 }
 
 }  // namespace
 
-static_assert(4 * kNormThreads * 8 == kMaxNormCols, "the longest row");
+static_assert(2 * kNormThreads * 8 == kMaxNormCols, "the longest row");
 
 hipError_t launch_rms_norm(const NormRows& a, const void* x, int64_t ld_x, const void* res, int64_t ld_res, float eps,
                            void* sum, int64_t ld_sum, float* rstd, hipStream_t st) {
@@ -378,7 +379,7 @@ hipError_t launch_rms_norm(const NormRows& a, const void* x, int64_t ld_x, const
 }
 
 // Rows that a block of the gradient works on at once.
-static int norm_rows_at_once(const NormShape& n) { return n.v == 1 ? kNormThreads1 / n.threads : 1; }
+static int norm_rows_at_once(const NormShape& n) { return n.v == 1 ? kNormThreads / n.threads : 1; }
 
 // One part for each block that runs at once (the registers leave room for 20 waves
 // a compute unit).
