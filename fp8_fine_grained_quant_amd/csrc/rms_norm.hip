@@ -104,11 +104,28 @@ __device__ __forceinline__ void store_quantized(const float (&y)[8], uint8_t* q,
   if ((piece & 15) == 0 && (piece >> 4) * 128 < cols) s[piece >> 4] = sc;
 }
 
-// Sum over a row's threads, `waves` waves from wave `first` of the block on, the
-// same bits in every thread.  `red` holds a value of each wave; the caller
-// alternates between two of them, so that one barrier a call is enough.
-__device__ __forceinline__ float norm_row_sum(float v, float* red, int first, int waves) {
+// Which rows a thread works on: a block has as many rows at once as its threads
+// hold (row_threads each).  NARROW: rows of 16 or 32 threads, several to a wave;
+// otherwise a row's threads are whole waves.
+template <bool NARROW>
+struct NormPlace {
+  int rows_at_once, mine, t;  // the block's rows, this thread's one among them, its place there
+  __device__ __forceinline__ explicit NormPlace(int row_threads) {
+    rows_at_once = (int)blockDim.x / row_threads;
+    mine = (int)threadIdx.x / row_threads;
+    if (!NARROW) mine = __builtin_amdgcn_readfirstlane(mine);
+    t = (int)threadIdx.x - mine * row_threads;
+  }
+};
+
+// Sum over a row's threads, the same bits in every thread.  Whole waves: `red`
+// holds a value of each wave of the block, and the caller alternates between two
+// of them, so that one barrier a call is enough.
+template <bool NARROW>
+__device__ __forceinline__ float norm_row_sum(float v, float* red, int mine, int row_threads) {
   v = row16_sum(v);
+  if (NARROW) return row_threads == 16 ? v : v + __shfl_xor(v, 16);
+  const int waves = row_threads >> 6, first = mine * waves;
   v += __shfl_xor(v, 16);
   v += __shfl_xor(v, 32);
   if (waves == 1) return v;
@@ -120,28 +137,33 @@ __device__ __forceinline__ float norm_row_sum(float v, float* red, int first, in
 }
 
 // NT: rows come and go past the caches (see past_caches).
-template <class Row, int V, bool TINY, int NT>
+template <class Row, int V, bool TINY, int NT, bool NARROW>
 __global__ __launch_bounds__(kNormThreads) void k_rms_norm(const NormRows a, const void* x_, int64_t ld_x,
-                                                                 const void* res_, int64_t ld_res, float eps,
-                                                                 void* sum_, int64_t ld_sum, float* rstd_out) {
+                                                           const void* res_, int64_t ld_res, float eps, void* sum_,
+                                                           int64_t ld_sum, float* rstd_out, int row_threads) {
   typedef typename Row::elem elem;
   __shared__ float red[2][16];
   const elem *x = (const elem*)x_, *res = (const elem*)res_;
   elem *y = (elem*)a.out, *sum = (elem*)sum_;
   const int cols = (int)a.cols;
+  const NormPlace<NARROW> at(row_threads);
   int piece[V], c0[V];
   bool whole[V];
   float w[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    piece[i] = i * (int)blockDim.x + (int)threadIdx.x;
+    piece[i] = i * row_threads + at.t;
     c0[i] = norm_col<Row>(piece[i]);
     whole[i] = no_cut<Row>(c0[i], cols, cols);
     if (V == 1) load_weights<Row>(a.w, c0[i], cols, w[i]);
   }
   const float inv_cols = 1.f / (float)cols;
   int turn = 0;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, turn ^= 1) {
+  for (int64_t r0 = (int64_t)blockIdx.x * at.rows_at_once; r0 < a.rows;
+       r0 += (int64_t)gridDim.x * at.rows_at_once, turn ^= 1) {
+    // rows past the last one repeat it and leave nothing
+    const bool on = r0 + at.mine < a.rows;
+    const int64_t r = on ? r0 + at.mine : a.rows - 1;
     typename Row::Raw raw[V], other[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) raw[i] = load_row_piece<Row, TINY, NT>(x + r * ld_x, c0[i], cols, whole[i]);
@@ -160,14 +182,15 @@ __global__ __launch_bounds__(kNormThreads) void k_rms_norm(const NormRows a, con
         for (int e = 0; e < 8; ++e) v[e] += o[e];
         raw[i] = Row::pack(v);
         Row::unpack(raw[i], v);
-        store_row_piece<Row, NT>(sum + r * ld_sum, c0[i], cols, whole[i], raw[i]);
+        if (on) store_row_piece<Row, NT>(sum + r * ld_sum, c0[i], cols, whole[i], raw[i]);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
     }
-    ss = norm_row_sum(ss, red[turn], 0, (int)blockDim.x >> 6);
+    ss = norm_row_sum<NARROW>(ss, red[turn], at.mine, row_threads);
+    if (!on) continue;
     const float rstd = 1.f / sqrtf(__builtin_fmaf(ss, inv_cols, eps));
-    if (threadIdx.x == 0) rstd_out[r] = rstd;
+    if (at.t == 0) rstd_out[r] = rstd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float v[8];
@@ -181,10 +204,8 @@ __global__ __launch_bounds__(kNormThreads) void k_rms_norm(const NormRows a, con
   }
 }
 
-// A block works on as many rows at once as its threads hold (row_threads each):
-// few columns leave a row with few threads, and a block's part of dw is written
-// once however many rows the block has.
-template <class Row, int V, bool TINY, int NT>
+// A block's part of dw is written once however many rows the block has.
+template <class Row, int V, bool TINY, int NT, bool NARROW>
 __global__ __launch_bounds__(kNormThreads) void k_rms_norm_bwd(const NormRows a, const void* dy_, int64_t ld_dy,
                                                                      const void* x_, int64_t ld_x, const float* rstd_in,
                                                                      const void* dsum_, int64_t ld_dsum,
@@ -195,16 +216,13 @@ __global__ __launch_bounds__(kNormThreads) void k_rms_norm_bwd(const NormRows a,
   const elem *dy = (const elem*)dy_, *x = (const elem*)x_, *dsum = (const elem*)dsum_;
   elem* dx = (elem*)a.out;
   const int cols = (int)a.cols;
-  // the block's rows and this thread's place among them (a row's threads are whole waves)
-  const int rows_at_once = V == 1 ? (int)blockDim.x / row_threads : 1;
-  const int mine = V == 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / row_threads) : 0;
-  const int t = (int)threadIdx.x - mine * row_threads;
+  const NormPlace<NARROW> at(row_threads);
   int piece[V], c0[V];
   bool whole[V];
   float w[V][8], dw[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    piece[i] = i * row_threads + t;
+    piece[i] = i * row_threads + at.t;
     c0[i] = norm_col<Row>(piece[i]);
     whole[i] = no_cut<Row>(c0[i], cols, cols);
     if (V == 1) load_weights<Row>(a.w, c0[i], cols, w[i]);
@@ -213,11 +231,10 @@ __global__ __launch_bounds__(kNormThreads) void k_rms_norm_bwd(const NormRows a,
   }
   const float inv_cols = 1.f / (float)cols;
   int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * rows_at_once; r0 < a.rows;
-       r0 += (int64_t)gridDim.x * rows_at_once, turn ^= 1) {
-    // rows past the last one repeat it and leave nothing
-    const bool on = r0 + mine < a.rows;
-    const int64_t r = on ? r0 + mine : a.rows - 1;
+  for (int64_t r0 = (int64_t)blockIdx.x * at.rows_at_once; r0 < a.rows;
+       r0 += (int64_t)gridDim.x * at.rows_at_once, turn ^= 1) {
+    const bool on = r0 + at.mine < a.rows;
+    const int64_t r = on ? r0 + at.mine : a.rows - 1;
     typename Row::Raw rx[V], rd[V], ro[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -244,7 +261,7 @@ __global__ __launch_bounds__(kNormThreads) void k_rms_norm_bwd(const NormRows a,
         c = __builtin_fmaf(p, w[i][e], c);
       }
     }
-    c = norm_row_sum(c, red[turn], mine * (row_threads >> 6), row_threads >> 6) * inv_cols;
+    c = norm_row_sum<NARROW>(c, red[turn], at.mine, row_threads) * inv_cols;
     if (!on) continue;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -263,14 +280,14 @@ __global__ __launch_bounds__(kNormThreads) void k_rms_norm_bwd(const NormRows a,
       if (a.q) store_quantized<Row>(vd, a.q + r * a.ld_q, a.s + r * a.ld_s, piece[i], c0[i], cols, whole[i]);
     }
   }
-  if (V == 1 && rows_at_once > 1) {
+  if (V == 1 && at.rows_at_once > 1) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) held[e][threadIdx.x] = dw[0][e];
     __syncthreads();
-    if (mine > 0) return;
-    for (int k = 1; k < rows_at_once; ++k)
+    if (at.mine > 0) return;
+    for (int k = 1; k < at.rows_at_once; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dw[0][e] += held[e][k * row_threads + t];
+      for (int e = 0; e < 8; ++e) dw[0][e] += held[e][k * row_threads + at.t];
   }
   part += (int64_t)blockIdx.x * cols;
 #pragma unroll
@@ -322,13 +339,13 @@ __global__ __launch_bounds__(kPartCols* kPartRuns) void k_norm_parts(const float
 struct NormShape {
   int v, threads;
 };
-// Pieces of 8 columns, 16 to a group of 128; as many threads as there are, up to
-// the block's most.
+// A row's pieces of 8 columns, 16 to a group of 128, and as many threads: a quarter
+// or half of a wave, or whole waves.
 NormShape norm_shape(int64_t cols) {
   const int64_t pieces = (cols + 127) / 128 * 16;
   NormShape n;
   n.v = pieces <= kNormThreads ? 1 : 2;
-  n.threads = (int)((pieces + 64 * n.v - 1) / (64 * n.v) * 64);
+  n.threads = pieces <= 32 ? (int)pieces : (int)((pieces + 64 * n.v - 1) / (64 * n.v) * 64);
   return n;
 }
 
@@ -348,16 +365,20 @@ bool past_caches(const NormRows& a, int matrices) {
   return a.rows * a.cols * (a.bf16 ? 2 : 4) * matrices > ((int64_t)512 << 20);
 }
 
-// fn(Row type, pieces per thread, a row may be shorter than a lane's run, past the caches)
+// fn(Row type, pieces per thread, a row may be shorter than a lane's run, past the
+// caches, rows narrower than a wave)
 template <class F>
-hipError_t norm_dispatch(const NormRows& a, int v, bool past, F fn) {
+hipError_t norm_dispatch(const NormRows& a, const NormShape& n, bool past, F fn) {
   auto with = [&](auto row) {
     typedef decltype(row) Row;
     typedef std::integral_constant<int, 0> Zero;
     typedef std::integral_constant<int, 1> One;
-    if (a.cols < Row::kLen) return fn(row, One{}, std::true_type{}, Zero{});
-    if (v == 1) return past ? fn(row, One{}, std::false_type{}, One{}) : fn(row, One{}, std::false_type{}, Zero{});
-    return fn(row, std::integral_constant<int, 2>{}, std::false_type{}, Zero{});
+    typedef std::true_type Yes;
+    typedef std::false_type No;
+    if (a.cols < Row::kLen) return fn(row, One{}, Yes{}, Zero{}, Yes{});
+    if (n.threads < 64) return past ? fn(row, One{}, No{}, One{}, Yes{}) : fn(row, One{}, No{}, Zero{}, Yes{});
+    if (n.v == 1) return past ? fn(row, One{}, No{}, One{}, No{}) : fn(row, One{}, No{}, Zero{}, No{});
+    return fn(row, std::integral_constant<int, 2>{}, No{}, Zero{}, No{});
   };
   return a.bf16 ? with(RowBF16{}) : with(RowF32{});
 }
@@ -369,11 +390,14 @@ static_assert(2 * kNormThreads * 8 == kMaxNormCols, "the longest row");
 hipError_t launch_rms_norm(const NormRows& a, const void* x, int64_t ld_x, const void* res, int64_t ld_res, float eps,
                            void* sum, int64_t ld_sum, float* rstd, hipStream_t st) {
   const NormShape n = norm_shape(a.cols);
-  const int64_t blocks = norm_blocks(a.rows, n.threads, 32);
+  const int at_once = n.threads < 64 ? 256 / n.threads : 1;
+  const int64_t blocks = norm_blocks((a.rows + at_once - 1) / at_once, n.threads * at_once, 32);
   const bool past = past_caches(a, 1 + (res ? 2 : 0) + (a.out ? 1 : 0));
-  return norm_dispatch(a, n.v, past, [&](auto row, auto v, auto tiny, auto nt) {
-    hipLaunchKernelGGL((k_rms_norm<decltype(row), decltype(v)::value, decltype(tiny)::value, decltype(nt)::value>),
-                       dim3((uint32_t)blocks), dim3(n.threads), 0, st, a, x, ld_x, res, ld_res, eps, sum, ld_sum, rstd);
+  return norm_dispatch(a, n, past, [&](auto row, auto v, auto tiny, auto nt, auto narrow) {
+    hipLaunchKernelGGL((k_rms_norm<decltype(row), decltype(v)::value, decltype(tiny)::value, decltype(nt)::value,
+                                   decltype(narrow)::value>),
+                       dim3((uint32_t)blocks), dim3(n.threads * at_once), 0, st, a, x, ld_x, res, ld_res, eps, sum,
+                       ld_sum, rstd, n.threads);
     return hipGetLastError();
   });
 }
@@ -396,8 +420,9 @@ hipError_t launch_rms_norm_bwd(const NormRows& a, const void* dy, int64_t ld_dy,
   const int64_t parts = rms_norm_parts(a.rows, a.cols);
   if (parts > 0) {
     const bool past = past_caches(a, 2 + (dsum ? 1 : 0) + (a.out ? 1 : 0));
-    const hipError_t err = norm_dispatch(a, n.v, past, [&](auto row, auto v, auto tiny, auto nt) {
-      hipLaunchKernelGGL((k_rms_norm_bwd<decltype(row), decltype(v)::value, decltype(tiny)::value, decltype(nt)::value>),
+    const hipError_t err = norm_dispatch(a, n, past, [&](auto row, auto v, auto tiny, auto nt, auto narrow) {
+      hipLaunchKernelGGL((k_rms_norm_bwd<decltype(row), decltype(v)::value, decltype(tiny)::value, decltype(nt)::value,
+                                         decltype(narrow)::value>),
                          dim3((uint32_t)parts), dim3(n.threads * norm_rows_at_once(n)), 0, st, a, dy, ld_dy, x, ld_x,
                          rstd, dsum, ld_dsum, part, n.threads);
       return hipGetLastError();
