@@ -31,7 +31,7 @@ LIB = os.path.join(HERE, "libfp8q.so")
 LIB_DEBUG = os.path.join(HERE, "libfp8q_debug.so")
 CALLS = os.path.join(HERE, "_calls.so")
 SOURCES = ["quant_kernels.hip", "quant_mx.hip", "gemm_fp8.hip", "gemm_mx.hip", "moe_route.hip", "moe_sort.hip", "moe_rows.hip",
-           "grad_clip.hip", "gemm_swiglu_few.hip", "rms_norm.hip", "adamw.hip", "api.cpp"]
+           "grad_clip.hip", "gemm_swiglu_few.hip", "gemm_gated_small.hip", "rms_norm.hip", "adamw.hip", "api.cpp"]
 ARCH = os.environ.get("FP8Q_ARCH", "gfx950")
 
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")

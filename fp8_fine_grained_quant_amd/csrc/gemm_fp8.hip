@@ -865,7 +865,7 @@ __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
           up[i][j][r] = acc[i][j + kTN / 2][r];
         }
     // (the block scales in LDS are not needed any more: room for the row maxima)
-    store_tile_swiglu<kTM>(gate, up, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 64, lane, sbk_all,
+    store_tile_swiglu<kTM, kTN / 2>(gate, up, ep + (w & 1) * 12288, p, tc.m0 + wr * 64, tc.mend, tc.n0 + wc * 64, lane, sbk_all,
                            wr * 64, wc);
   } else if constexpr (EPI == kEpiDSwiglu) {
     static_assert(!OUT_F32, "gated block's gradient: BF16 Dgrad only");
@@ -1184,6 +1184,9 @@ hipError_t launch_gemm_interval(const GemmArgs& a, int chunks, hipStream_t st) {
 static hipError_t launch_gated(const GemmArgs& a, bool sc4, hipStream_t st) {
   const bool grouped = a.offsets != nullptr;
   const int64_t tm = (a.M + kBM - 1) / kBM + (grouped ? a.E : 0);  // grouped: upper bound
+  if (int rows = 0; !grouped && gemm_tile_setting() == 0 && gated_small_time(a.M, a.N, a.K, a.gated, &rows) <
+                                                                gated_large_time(a.M, a.N, a.K, a.gated))
+    return launch_gated_small(a, rows, st);
   if (a.gated == kSwiglu) {
     const dim3 grid((uint32_t)(tm * (a.N / (kWBN / 2))));
     if (grouped) {

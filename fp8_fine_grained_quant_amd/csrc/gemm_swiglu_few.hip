@@ -218,14 +218,17 @@ int few_tiles(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : M <= 64 ? 4 : 8; }
 
 }  // namespace
 
-// The times of both kernels in ns, of rounds of workgroups: here 4 us and 40 + 31
-// mt ns a chunk (8, 32, 64 and 128 rows of 2048 x 7168: 7.3, 8.7, 12.1 and 19.4 us),
-// the 256-row tiles 9 us and 1.1 a chunk (up to 256 rows there 70 us, of 8192 x
-// 4096 44).
+// By the times of the kernels in ns, of rounds of workgroups: here 4 us and 40 + 31
+// mt ns a chunk (8, 32, 64 and 128 rows of 2048 x 7168: 7.3, 8.7, 12.1 and 19.4 us;
+// tiles of 32 rows take 28 there up to 256 rows, the large ones 50 to 70).  Up to 16
+// rows the small tiles are not asked: what is generated for a few sequences has the
+// exact products' accuracy.
 bool swiglu_few(int64_t M, int64_t N, int64_t K) {
   const int64_t mt = few_tiles(M), nk = K / 128, cus = device_cu_count();
-  auto rounds = [&](int64_t row_tile, int64_t cols) { return ((M + row_tile - 1) / row_tile * (N / cols) + cus - 1) / cus; };
-  return rounds(16 * mt, kFewCols) * (4000 + nk * (40 + 31 * mt)) <= rounds(256, 128) * (8700 + 1100 * nk);
+  const int64_t rounds = ((M + 16 * mt - 1) / (16 * mt) * (N / kFewCols) + cus - 1) / cus;
+  const int64_t here = rounds * (4000 + nk * (40 + 31 * mt));
+  int rows;
+  return here <= gated_large_time(M, N, K, kSwiglu) && (M <= 16 || here <= gated_small_time(M, N, K, kSwiglu, &rows));
 }
 
 // The codes of a 128-column group need 16 workgroups' outputs: they are made by

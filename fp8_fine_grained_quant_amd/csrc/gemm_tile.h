@@ -320,60 +320,64 @@ __device__ __forceinline__ void store_bf16(const float (&v)[TM][TN][4], uint8_t*
   }
 }
 
-// One wave's gate and up accumulators of the same WM x 64 outputs (layout of
+// One wave's gate and up accumulators of the same 16 TM x 16 TN outputs (layout of
 // store_tile with TRL = 1): gate and up as they are to p.gu (BF16, up N columns
 // after gate) if given, h to p.C (BF16) if given, and h's codes and scales,
-// over the unrounded values, to p.qo and p.so if given.  A 128-column group's
-// two halves are held by two waves, which exchange their rows' max-abs through
-// `half_max` [2][256]: with p.qo every wave of the workgroup makes this call.
-// row_in_tile is the strip's first row in the tile, half the wave's half.
-template <int TM>
-__device__ __forceinline__ void store_tile_swiglu(float (&g)[TM][4][4], const float (&u)[TM][4][4], uint8_t* ep,
+// over the unrounded values, to p.qo and p.so if given.  A 128-column group is
+// held by 8 / TN waves, which exchange their rows' max-abs through
+// `maxima` [8 / TN][256]: with p.qo every wave of the workgroup makes this call.
+// row_in_tile is the strip's first row in the tile, part the wave's part of the group.
+template <int TM, int TN>
+__device__ __forceinline__ void store_tile_swiglu(float (&g)[TM][TN][4], const float (&u)[TM][TN][4], uint8_t* ep,
                                                   const GemmArgs& p, int64_t row0, int64_t mend, int col0, int lane,
-                                                  float* half_max, int row_in_tile, int half) {
+                                                  float* maxima, int row_in_tile, int part) {
   const int lg = lane >> 4, l16 = lane & 15;
   if (p.gu != nullptr) {
-    store_bf16<TM, 4>(g, ep, p.gu + col0, p.ld_gu, row0, mend, lane);
-    store_bf16<TM, 4>(u, ep, p.gu + col0 + p.N, p.ld_gu, row0, mend, lane);
+    store_bf16<TM, TN>(g, ep, p.gu + col0, p.ld_gu, row0, mend, lane);
+    store_bf16<TM, TN>(u, ep, p.gu + col0 + p.N, p.ld_gu, row0, mend, lane);
   }
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) g[i][j][r] = g[i][j][r] * sigmoid_f32(g[i][j][r]) * u[i][j][r];
-  if (p.C != nullptr) store_bf16<TM, 4>(g, ep, reinterpret_cast<uint16_t*>(p.C) + col0, p.ldc, row0, mend, lane);
+  if (p.C != nullptr) store_bf16<TM, TN>(g, ep, reinterpret_cast<uint16_t*>(p.C) + col0, p.ldc, row0, mend, lane);
   if (p.qo == nullptr) return;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r) m = max(m, abs_bits(g[i][j][r]));
     m = max(m, (uint32_t)__shfl_xor((int)m, 16));  // the row's other three lanes
     m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-    if (lg == 0) half_max[half * 256 + row_in_tile + 16 * i + l16] = __uint_as_float(m);
+    if (lg == 0) maxima[part * 256 + row_in_tile + 16 * i + l16] = __uint_as_float(m);
   }
   __syncthreads();  // (the staging area is read out as well)
-  constexpr int P = 64 + 16;  // padded LDS row pitch of the codes
+  constexpr int P = 16 * TN + 16;     // padded LDS row pitch of the codes
+  constexpr int RPI = 64 / TN;        // rows per store instruction, of TN 16-byte segments
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int rt = row_in_tile + 16 * i + l16;
     float sc, inv;
-    group_scale(__builtin_fmaxf(half_max[rt], half_max[256 + rt]), sc, inv);
-    const int64_t row = row0 + 16 * i + l16;
-    if (half == 0 && lg == 0 && row < mend) p.so[row * p.ld_so + (col0 >> 7)] = sc;
+    float most = maxima[rt];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int k = 1; k < 8 / TN; ++k) most = __builtin_fmaxf(most, maxima[256 * k + rt]);
+    group_scale(most, sc, inv);
+    const int64_t row = row0 + 16 * i + l16;
+    if (part == 0 && lg == 0 && row < mend) p.so[row * p.ld_so + (col0 >> 7)] = sc;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
       *reinterpret_cast<uint32_t*>(ep + (16 * i + l16) * P + 16 * j + 4 * lg) =
           pack4_e4m3_grp(g[i][j][0] * inv, g[i][j][1] * inv, g[i][j][2] * inv, g[i][j][3] * inv);
   }
   __builtin_amdgcn_s_waitcnt(0xC07F);
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
-  for (int it = 0; it < TM; ++it) {  // 16 rows of four 16-byte segments
-    const int rl = it * 16 + (lane >> 2), ch = lane & 3;
+  for (int it = 0; it < 16 * TM / RPI; ++it) {
+    const int rl = it * RPI + lane / TN, ch = lane % TN;
     const int64_t row = row0 + rl;
     if (row >= mend) continue;
     const uint4 v = *reinterpret_cast<const uint4*>(ep + rl * P + 16 * ch);

@@ -705,8 +705,8 @@ int64_t fp8q_rms_norm_bwd_workspace(int64_t rows, int64_t cols);
  *            on the current device
  * g and u have the accuracy of fp8q_gemm_fprop.  Where few rows would leave most of
  * the device without a tile, a kernel for few rows runs, with the accuracy of
- * fp8q_gemm_fprop_exact (by the sizes and the device's compute units alone: up to
- * 384 rows of a block of width 2048, up to 16 of any below 20000).
+ * fp8q_gemm_fprop_exact (by the sizes and the device's compute units alone: with
+ * K = 7168 up to 128 rows of a block of width 2048 and up to 16 of one of 16384).
  * Rules: N % 128 == 0, K % 128 == 0, K <= 131072, any M >= 0; xq, wq, h, gu, q
  * 16-byte aligned with row strides that are multiples of 16 bytes.
  */

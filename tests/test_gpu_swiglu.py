@@ -84,6 +84,30 @@ def test_both_kernels_are_taken():
     assert {few(*c) for c in DENSE if c[0] > 64} == {few(*c) for c in DENSE if c[0] <= 64} == {True, False}
 
 
+def with_large_tiles(run):
+    fq.set_gemm_tile("256x128")
+    try:
+        return run()
+    finally:
+        fq.set_gemm_tile("auto")
+
+
+@pytest.mark.parametrize("chunks", list(range(1, 15)) + [56])
+@pytest.mark.parametrize("m, f", [(700, 1024), (1000, 2048), (1025, 2048)])
+def test_small_and_large_tiles_agree(m, f, chunks):
+    """Tiles of every height (32, 64 and 128 rows, by the sizes) give the large
+    ones' bits, for every number of chunks that the pipeline ends with."""
+    k = 128 * chunks
+    ops = operands(m, f, k)
+    both = [run() for run in (lambda: fq.gemm_swiglu_quant(*ops, with_output=True, with_gu=True),
+                              lambda: with_large_tiles(lambda: fq.gemm_swiglu_quant(*ops, with_output=True, with_gu=True)))]
+    assert all(torch.equal(a, b) for a, b in zip(*both))
+    dyq, dys, wt, ws, gu = gradient_operands(m, k, f)
+    small = fq.gemm_dgrad_swiglu(dyq, dys, wt, ws, gu, with_h=True)
+    large = with_large_tiles(lambda: fq.gemm_dgrad_swiglu(dyq, dys, wt, ws, gu, with_h=True))
+    assert all(torch.equal(a, b) for a, b in zip(small, large))
+
+
 def offsets_of(counts):
     return torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device=DEV)
 
