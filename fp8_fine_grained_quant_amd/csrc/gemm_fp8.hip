@@ -1184,8 +1184,9 @@ hipError_t launch_gemm_interval(const GemmArgs& a, int chunks, hipStream_t st) {
 static hipError_t launch_gated(const GemmArgs& a, bool sc4, hipStream_t st) {
   const bool grouped = a.offsets != nullptr;
   const int64_t tm = (a.M + kBM - 1) / kBM + (grouped ? a.E : 0);  // grouped: upper bound
-  if (int rows = 0; !grouped && gemm_tile_setting() == 0 && gated_small_time(a.M, a.N, a.K, a.gated, &rows) <
-                                                                gated_large_time(a.M, a.N, a.K, a.gated))
+  const int64_t experts = grouped ? a.E : 0;
+  if (int rows = 0; gemm_tile_setting() == 0 && gated_small_time(a.M, a.N, a.K, experts, a.gated, &rows) <
+                                                    gated_large_time(a.M, a.N, a.K, experts, a.gated))
     return launch_gated_small(a, rows, st);
   if (a.gated == kSwiglu) {
     const dim3 grid((uint32_t)(tm * (a.N / (kWBN / 2))));

@@ -1,5 +1,5 @@
-// The gated feed-forward block and its gradient of a few hundred rows (gfx950):
-// too many for the kernel of few rows, and too few for the 256-row tiles to give
+// The gated feed-forward block and its gradient of a few hundred rows (gfx950),
+// in all or an expert: too many for the kernel of few rows, and too few for the 256-row tiles to give
 // every compute unit one.
 //
 // Tiles of 16 TM rows (32, 64 or 128) by 64 TN rows of B: of the block TN is 4, 128
@@ -27,6 +27,8 @@
 #include "gemm_tile.h"
 #include "launch.h"
 
+#include <algorithm>
+
 namespace fp8q {
 
 namespace {
@@ -37,7 +39,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 
 constexpr int kSmallNT = 256;
 
-template <bool GRADIENT, int TM>
+template <bool GRADIENT, int TM, bool GROUPED>
 __global__ __launch_bounds__(kSmallNT) void k_gated_small(const GemmArgs p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int TN = GRADIENT ? 2 : 4, BM = 16 * TM;
@@ -46,10 +48,12 @@ __global__ __launch_bounds__(kSmallNT) void k_gated_small(const GemmArgs p) {
   // one LDS object a stage, so that no wait for one covers another
   __shared__ __attribute__((aligned(16))) uint8_t st0[kStage], st1[kStage], st2[kStage];
   TileCoord tc;
-  tile_coord<BM, 128, false>(p, tc);
+  if (!tile_coord<BM, 128, GROUPED>(p, tc)) return;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int nk = (int)(p.K / 128), rows = (int)min(p.M - tc.m0, (int64_t)BM);
+  const int nk = (int)(p.K / 128), rows = (int)min(tc.mend - tc.m0, (int64_t)BM);
+  const uint8_t* const B = p.B + (GROUPED ? tc.e * p.b_estride : 0);
+  const float* const sb = p.sb + (GROUPED ? tc.e * p.sb_estride : 0);
 
   auto rsrc = [](const void* base, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
@@ -59,10 +63,10 @@ __global__ __launch_bounds__(kSmallNT) void k_gated_small(const GemmArgs p) {
   const int64_t b0 = GRADIENT ? tc.n0 + 32 * w : tc.n0 + 64 * (w & 1) + (w >> 1) * p.N;
   const int64_t s0 = GRADIENT || w == 2 ? tc.n0 : tc.n0 + p.N;
   const __amdgpu_buffer_rsrc_t rA = rsrc(p.A + tc.m0 * p.lda, (uint32_t)(rows * p.lda));  // rows past the last one: no access
-  const __amdgpu_buffer_rsrc_t rB = rsrc(p.B + b0 * p.ldb, (uint32_t)(16 * TN * p.ldb));
+  const __amdgpu_buffer_rsrc_t rB = rsrc(B + b0 * p.ldb, (uint32_t)(16 * TN * p.ldb));
   const __amdgpu_buffer_rsrc_t rS =
       w < 2 ? rsrc(p.sa + tc.m0 * p.ld_sa, (uint32_t)(rows * p.ld_sa * 4))
-            : rsrc(p.sb + s0 / 128 * p.sb_rs, (uint32_t)(((int64_t)(nk - 1) * p.sb_cs + 1) * 4));
+            : rsrc(sb + s0 / 128 * p.sb_rs, (uint32_t)(((int64_t)(nk - 1) * p.sb_cs + 1) * 4));
   const int r8 = lane >> 3, c16 = 16 * ((lane & 7) ^ r8);
   const uint32_t vA = (uint32_t)((w * kIA * 8 + r8) * p.lda + c16), vB = (uint32_t)(r8 * p.ldb + c16);
   const uint32_t stepA = (uint32_t)(8 * p.lda), stepB = (uint32_t)(8 * p.ldb);
@@ -233,28 +237,58 @@ __global__ __launch_bounds__(kSmallNT) void k_gated_small(const GemmArgs p) {
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
-template <bool GRADIENT, int TM>
+template <bool GRADIENT, int TM, bool GROUPED>
 hipError_t small(const GemmArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_gated_small<GRADIENT, TM>), dim3((uint32_t)((a.M + 16 * TM - 1) / (16 * TM) * (a.N / 128))),
-                     dim3(kSmallNT), 0, st, a);
+  const int64_t tiles_m = (a.M + 16 * TM - 1) / (16 * TM) + (GROUPED ? a.E : 0);  // grouped: upper bound
+  hipLaunchKernelGGL((k_gated_small<GRADIENT, TM, GROUPED>), dim3((uint32_t)(tiles_m * (a.N / 128))), dim3(kSmallNT), 0,
+                     st, a);
   return hipGetLastError();
+}
+template <bool GRADIENT, bool GROUPED>
+hipError_t small(const GemmArgs& a, int rows, hipStream_t st) {
+  return rows == 32   ? small<GRADIENT, 2, GROUPED>(a, st)
+         : rows == 64 ? small<GRADIENT, 4, GROUPED>(a, st)
+                      : small<GRADIENT, 8, GROUPED>(a, st);
+}
+
+// What a kernel's workgroups take, in ns: a start, and a chunk's time, which grows by
+// `full` where every compute unit has one.
+struct TileTime {
+  int rows, cols, start, chunk, full;
+};
+// About how many there are: an expert's last tile of rows is half full on average,
+// and no expert has none.
+int64_t tile_count(const TileTime& t, int64_t M, int64_t N, int64_t experts) {
+  int64_t tiles_m = (M + t.rows - 1) / t.rows;
+  if (experts > 0) tiles_m = std::min(M, std::max(experts, tiles_m + experts / 2));
+  return tiles_m * (N / t.cols);
+}
+int64_t tile_time(const TileTime& t, int64_t tiles, int64_t nk) {
+  const int64_t cus = device_cu_count(), rounds = tiles / cus, rest = tiles % cus;
+  return rounds * (t.start + nk * (t.chunk + t.full)) + (rest ? t.start + nk * (t.chunk + t.full * rest / cus) : 0);
 }
 
 }  // namespace
 
-// Times in ns: rounds of workgroups, a launch and its epilogue, and a chunk.
 // Measured, of 2048 x 7168 with gate and up kept: tiles of 32 rows (512 rows) 31 us,
-// of 64 (1024) 38, of 128 (2048) 64, the large tiles 74, 75 and 77; the gradient's
-// 20, 27 and 43, the large ones 55, 57 and 60.  4096 rows: 128 and 101, 85 and 71.
-int64_t gated_small_time(int64_t M, int64_t N, int64_t K, int gated, int* rows) {
-  static constexpr struct {
-    int rows, start[2], chunk[2];  // of the block, of the gradient
-  } kTiles[3] = {{32, {5100, 4900}, {420, 240}}, {64, {6200, 5700}, {490, 320}}, {128, {8200, 8500}, {850, 550}}};
-  const int64_t nk = K / 128, cus = device_cu_count(), g = gated == kDSwiglu;
+// of 64 (1024) 38, of 128 (2048) 62, the large tiles 72, 75 and 76; the gradient's
+// 20, 26 and 41, the large ones 55, 57 and 59.  4096 rows: 128 and 97, 85 and 69.
+int64_t gated_small_time(int64_t M, int64_t N, int64_t K, int64_t experts, int gated, int* rows) {
+  static constexpr TileTime kBlock[3] = {
+      {32, 128, 5100, 420, 40}, {64, 128, 6200, 490, 70}, {128, 128, 8200, 800, 150}};
+  static constexpr TileTime kGradient[3] = {
+      {32, 128, 4900, 235, 40}, {64, 128, 5700, 320, 50}, {128, 128, 8500, 500, 80}};
   int64_t best = INT64_MAX;
-  for (const auto& t : kTiles) {
-    const int64_t rounds = ((M + t.rows - 1) / t.rows * (N / 128) + cus - 1) / cus;
-    const int64_t time = rounds * (t.start[g] + nk * t.chunk[g]);
+  *rows = 0;
+  // Many experts' weights are a matter of the memory, which more tiles of rows ask for
+  // them more often: here up to two rounds of the lowest tiles (32 experts of 2048 x
+  // 7168: 256 rows in all 158 us, 184 with the large tiles; 1024 rows, in 3 rounds, 205
+  // and 196; 2048 rows 231 and 205.  8 experts of 1024 x 2048, 1000 rows: 15 and 30).
+  if (experts > 0 && tile_count(kBlock[0], M, N, experts) > 2 * device_cu_count()) return best;
+  for (const TileTime& t : gated == kSwiglu ? kBlock : kGradient) {
+    // a launch's threads are counted in 32 bits
+    if (((M + t.rows - 1) / t.rows + experts) * (N / t.cols) > ((int64_t(1) << 32) - 1) / kSmallNT) continue;
+    const int64_t time = tile_time(t, tile_count(t, M, N, experts), K / 128);
     if (time < best) {
       best = time;
       *rows = t.rows;
@@ -263,19 +297,19 @@ int64_t gated_small_time(int64_t M, int64_t N, int64_t K, int gated, int* rows) 
   return best;
 }
 
-int64_t gated_large_time(int64_t M, int64_t N, int64_t K, int gated) {
-  const int64_t nk = K / 128, cus = device_cu_count(), tiles_m = (M + 255) / 256;
-  auto rounds = [&](int64_t cols) { return (tiles_m * (N / cols) + cus - 1) / cus; };
-  if (gated == kSwiglu) return rounds(128) * (8700 + 1100 * nk);
-  // (the 256 x 256 tiles where they are taken)
-  return N % 256 == 0 && 2 * tiles_m * (N / 256) > cus ? rounds(256) * (15000 + 1300 * nk)
-                                                       : rounds(128) * (13000 + 730 * nk);
+int64_t gated_large_time(int64_t M, int64_t N, int64_t K, int64_t experts, int gated) {
+  // (the gradient's 256 x 256 tiles where they are taken)
+  const bool wide = N % 256 == 0 && 2 * ((M + 255) / 256) * (N / 256) > device_cu_count();
+  const TileTime t = gated == kSwiglu ? TileTime{256, 128, 8700, 1100, 500}
+                     : wide           ? TileTime{256, 256, 15000, 1300, 700}
+                                      : TileTime{256, 128, 13000, 730, 280};
+  return tile_time(t, tile_count(t, M, N, experts), K / 128);
 }
 
 hipError_t launch_gated_small(const GemmArgs& a, int rows, hipStream_t st) {
-  if (a.gated == kSwiglu)
-    return rows == 32 ? small<false, 2>(a, st) : rows == 64 ? small<false, 4>(a, st) : small<false, 8>(a, st);
-  return rows == 32 ? small<true, 2>(a, st) : rows == 64 ? small<true, 4>(a, st) : small<true, 8>(a, st);
+  const bool grouped = a.offsets != nullptr;
+  if (a.gated == kSwiglu) return grouped ? small<false, true>(a, rows, st) : small<false, false>(a, rows, st);
+  return grouped ? small<true, true>(a, rows, st) : small<true, false>(a, rows, st);
 }
 
 }  // namespace fp8q

@@ -228,7 +228,8 @@ bool swiglu_few(int64_t M, int64_t N, int64_t K) {
   const int64_t rounds = ((M + 16 * mt - 1) / (16 * mt) * (N / kFewCols) + cus - 1) / cus;
   const int64_t here = rounds * (4000 + nk * (40 + 31 * mt));
   int rows;
-  return here <= gated_large_time(M, N, K, kSwiglu) && (M <= 16 || here <= gated_small_time(M, N, K, kSwiglu, &rows));
+  return here <= gated_large_time(M, N, K, 0, kSwiglu) &&
+         (M <= 16 || here <= gated_small_time(M, N, K, 0, kSwiglu, &rows));
 }
 
 // The codes of a 128-column group need 16 workgroups' outputs: they are made by

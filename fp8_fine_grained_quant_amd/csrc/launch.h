@@ -125,8 +125,9 @@ hipError_t launch_swiglu_few(const GemmArgs& a, float* hf, hipStream_t st);
 hipError_t launch_gated_small(const GemmArgs& a, int rows, hipStream_t st);
 // About what it takes on the current device, and the tiles' rows for that; and what
 // the tiles of 256 rows take.
-int64_t gated_small_time(int64_t M, int64_t N, int64_t K, int gated, int* rows);
-int64_t gated_large_time(int64_t M, int64_t N, int64_t K, int gated);
+// (experts: 0 of dense rows)
+int64_t gated_small_time(int64_t M, int64_t N, int64_t K, int64_t experts, int gated, int* rows);
+int64_t gated_large_time(int64_t M, int64_t N, int64_t K, int64_t experts, int gated);
 
 // Microscaling (MXFP8 E4M3) quantizers: one E8M0 scale byte per 32
 // consecutive elements, along rows (quant_mx) or along columns with the

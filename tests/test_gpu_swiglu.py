@@ -132,6 +132,20 @@ def test_block_by_expert(counts, f, k):
     assert torch.equal(fq.grouped_gemm_swiglu(xq, xs, wq, ws, off)[0], h)
 
 
+@pytest.mark.parametrize("f, k", [(128, 128), (512, 640), (1024, 1792)])
+@pytest.mark.parametrize("counts", [[1] * 20, [33, 0, 64, 65, 1], [130, 0, 0, 200, 100, 70], [0, 500, 3, 0]], ids=str)
+def test_small_and_large_tiles_agree_by_expert(counts, f, k):
+    m, e, off = sum(counts), len(counts), offsets_of(counts)
+    ops = operands(m, f, k, e)
+    grads = gradient_operands(m, k, f, e)
+
+    def run():
+        return (*fq.grouped_gemm_swiglu_quant(*ops, off, with_output=True, with_gu=True),
+                *fq.grouped_gemm_dgrad_swiglu(*grads[:4], off, grads[4], with_h=True))
+
+    assert all(torch.equal(a, b) for a, b in zip(run(), with_large_tiles(run)))
+
+
 def gradient_operands(m, n, f, experts=0, seed=3):
     """dY's codes [m, n], the output projections' transposed codes [f, e n] and gu [m, 2f]."""
     g = torch.Generator().manual_seed(seed)
