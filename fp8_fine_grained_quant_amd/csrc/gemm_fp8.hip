@@ -595,7 +595,7 @@ static_assert(4 * kBM * kBK + 4 * 2 * kMaxChunks + 4 * 2 * 256 * 4 + 1024 <= 160
 // (scale rows that are not 16-byte aligned): the row scales come 4 bytes per row
 // and chunk, into a ring of 8 chunks.  4096 x 2048 x 7168 with gate and up kept:
 // 101 us, 2.4 PFLOP/s (the same product alone, 4096 x 4096 x 7168: 96 to 101);
-// 16384 rows over 32 experts 495 us (512 where a strip without rows was worked on
+// 16384 rows over 32 experts 533 us (552 where a strip without rows was worked on
 // like the others).
 template <int OUT_F32, bool GROUPED, int EPI, bool SC4 = true>
 __global__ __launch_bounds__(kWNT) void k_gemm_fp8_wide(GemmArgs p) {
