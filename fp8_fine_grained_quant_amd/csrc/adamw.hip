@@ -17,9 +17,12 @@
 // Bound by memory: every value is read and written once, 28 bytes an element
 // with FP32 gradients and states, 16.1 with 8-bit states and two more for a BF16
 // copy.  Parameters, gradients, copies and FP32 states pass the caches: 235M
-// parameters with 8-bit states and copies 815 us, 5.2 TB/s (871 through them,
-// 850 with only the stores past them); 200M with FP32 states 1124 us, 5.3 TB/s
-// (1179).
+// parameters with 8-bit states and copies 728 us, 5.9 TB/s (790 through them,
+// 770 with only the stores past them); 200M with FP32 states 972 us, 5.8 TB/s
+// (1043).  A block has one piece of a tensor, 8 elements a thread, and ends: what
+// the device holds is then made up by the pieces that begin as others end (2048
+// blocks that took 8192 elements at a time: 816 and 1045 us; 200 tensors of 100 to
+// 2000000 elements 160 us against 139, whose last blocks ran alone).
 
 #include "launch.h"
 #include "row_io.h"
@@ -29,7 +32,7 @@ namespace fp8q {
 namespace {
 
 constexpr int kAdamThreads = 256;
-static_assert(kAdamStep == kAdamThreads * 8 && kAdamStep % 128 == 0, "a step is 8 elements of every thread, whole groups");
+static_assert(kAdamChunk == kAdamThreads * 8 && kAdamChunk % 128 == 0, "8 elements of every thread, whole groups");
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x6C8E9CF5u;
@@ -142,89 +145,83 @@ __global__ __launch_bounds__(kAdamThreads) void k_adamw(const AdamTable<N> t, co
   // tensor has that of the one behind it, which is found)
   const int lane = threadIdx.x & 63;
   const int first = lane < t.n ? t.cum[lane < N ? lane : 0] : 0x7FFFFFFF;
-  const int chunks = t.cum[t.n];
   const double norm = a.norm ? (double)*a.norm : 0.0;
   const double factor = norm <= a.max_norm ? 1.0 : a.max_norm / norm;  // a NaN norm gives a NaN factor
-  const int at0 = ((int)threadIdx.x >> 4) * 128 + ((int)threadIdx.x & 15) * 4;
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = __popcll(__ballot(first <= c)) - 1;
-    const int64_t lo = (int64_t)(c - t.cum[i]) * a.chunk;
-    const int len = c + 1 < t.cum[i + 1] ? a.chunk : (int)t.last[i];
-    const uint32_t key = mix(mix(a.seed_lo + 0x9E3779B1u * (a.place + (uint32_t)i)) + a.seed_hi) +
-                         (uint32_t)((uint64_t)lo >> 32) * 0x27D4EB2Fu;
-    for (int step = 0; step < len; step += kAdamStep) {
-      const int at = step + at0;
-      if (step + ((int)threadIdx.x >> 4) * 128 >= len) break;  // a group's 16 lanes stay together
-      float p[8], g[8], m[8], v[8];
+  const int at = ((int)threadIdx.x >> 4) * 128 + ((int)threadIdx.x & 15) * 4;
+  const int c = blockIdx.x, i = __popcll(__ballot(first <= c)) - 1;
+  const int64_t lo = (int64_t)(c - t.cum[i]) * kAdamChunk;
+  const int len = c + 1 < t.cum[i + 1] ? kAdamChunk : (int)t.last[i];
+  const uint32_t key = mix(mix(a.seed_lo + 0x9E3779B1u * (a.place + (uint32_t)i)) + a.seed_hi) +
+                       (uint32_t)((uint64_t)lo >> 32) * 0x27D4EB2Fu;
+  if (((int)threadIdx.x >> 4) * 128 >= len) return;  // a group's 16 lanes stay together
+  float p[8], g[8], m[8], v[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t o = lo + at + 64 * h;
-        const int n = len - at - 64 * h;
-        load_f32(t.p[i] + o, n, p + 4 * h);
-        if (G_BF16) load_bf16((const uint16_t*)t.g[i] + o, n, g + 4 * h);
-        else load_f32((const float*)t.g[i] + o, n, g + 4 * h);
-        if (!BITS8) {
-          load_f32((const float*)t.m[i] + o, n, m + 4 * h);
-          load_f32((const float*)t.v[i] + o, n, v + 4 * h);
-        }
+  for (int h = 0; h < 2; ++h) {
+    const int64_t o = lo + at + 64 * h;
+    const int n = len - at - 64 * h;
+    load_f32(t.p[i] + o, n, p + 4 * h);
+    if (G_BF16) load_bf16((const uint16_t*)t.g[i] + o, n, g + 4 * h);
+    else load_f32((const float*)t.g[i] + o, n, g + 4 * h);
+    if (!BITS8) {
+      load_f32((const float*)t.m[i] + o, n, m + 4 * h);
+      load_f32((const float*)t.v[i] + o, n, v + 4 * h);
+    }
+  }
+  const int64_t group = (lo + at) >> 7;
+  if (BITS8) {
+    const float sm = t.m_scale[i][group], sv = t.v_scale[i][group];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t o = lo + at + 64 * h;
+      const int n = len - at - 64 * h;
+      decode4(load_code4((const uint8_t*)t.m[i] + o, n), sm, m + 4 * h);
+      decode4(load_code4((const uint8_t*)t.v[i] + o, n), sv, v + 4 * h);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (BITS8) v[e] *= v[e];
+    if (a.norm) g[e] = (float)((double)g[e] * factor);
+    // every product and sum rounded on its own: a state in 8 bits goes by the
+    // last bits of its value where that is near a border of the rounding, and
+    // these are the bits that the formula gives, term by term
+    m[e] = a.beta1 * m[e] + a.rest1 * g[e];
+    v[e] = a.beta2 * v[e] + a.rest2 * (g[e] * g[e]);
+    const float root = sqrtf(v[e]);
+    p[e] = __builtin_fmaf(p[e], a.keep, -(a.step * m[e] / __builtin_fmaf(root, a.root, a.eps)));
+    if (BITS8) v[e] = root;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t o = lo + at + 64 * h;
+    const int n = len - at - 64 * h;
+    store_f32(t.p[i] + o, n, p + 4 * h);
+    if (t.copy[i]) store_bf16(t.copy[i] + o, n, p + 4 * h);
+    if (!BITS8) {
+      store_f32((float*)t.m[i] + o, n, m + 4 * h);
+      store_f32((float*)t.v[i] + o, n, v + 4 * h);
+    }
+  }
+  if (BITS8) {
+    float inv_m, inv_v;
+    const float sm = state_scale(m, inv_m), sv = state_scale(v, inv_v);
+    if ((threadIdx.x & 15) == 0) {
+      t.m_scale[i][group] = sm;
+      t.v_scale[i][group] = sv;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t o = lo + at + 64 * h;
+      const int n = len - at - 64 * h;
+      float ym[4], yv[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t r = mix((uint32_t)(o + e) * 0x85297A4Du + key);
+        ym[e] = round_e4m3<false>(m[4 * h + e] * inv_m, (float)(r & 0xFFFFu) * 0x1p-16f);
+        yv[e] = round_e4m3<true>(v[4 * h + e] * inv_v, (float)(r >> 16) * 0x1p-16f);
       }
-      const int64_t group = (lo + at) >> 7;
-      if (BITS8) {
-        const float sm = t.m_scale[i][group], sv = t.v_scale[i][group];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t o = lo + at + 64 * h;
-          const int n = len - at - 64 * h;
-          decode4(load_code4((const uint8_t*)t.m[i] + o, n), sm, m + 4 * h);
-          decode4(load_code4((const uint8_t*)t.v[i] + o, n), sv, v + 4 * h);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (BITS8) v[e] *= v[e];
-        if (a.norm) g[e] = (float)((double)g[e] * factor);
-        // every product and sum rounded on its own: a state in 8 bits goes by the
-        // last bits of its value where that is near a border of the rounding, and
-        // these are the bits that the formula gives, term by term
-        m[e] = a.beta1 * m[e] + a.rest1 * g[e];
-        v[e] = a.beta2 * v[e] + a.rest2 * (g[e] * g[e]);
-        const float root = sqrtf(v[e]);
-        p[e] = __builtin_fmaf(p[e], a.keep, -(a.step * m[e] / __builtin_fmaf(root, a.root, a.eps)));
-        if (BITS8) v[e] = root;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t o = lo + at + 64 * h;
-        const int n = len - at - 64 * h;
-        store_f32(t.p[i] + o, n, p + 4 * h);
-        if (t.copy[i]) store_bf16(t.copy[i] + o, n, p + 4 * h);
-        if (!BITS8) {
-          store_f32((float*)t.m[i] + o, n, m + 4 * h);
-          store_f32((float*)t.v[i] + o, n, v + 4 * h);
-        }
-      }
-      if (BITS8) {
-        float inv_m, inv_v;
-        const float sm = state_scale(m, inv_m), sv = state_scale(v, inv_v);
-        if ((threadIdx.x & 15) == 0) {
-          t.m_scale[i][group] = sm;
-          t.v_scale[i][group] = sv;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t o = lo + at + 64 * h;
-          const int n = len - at - 64 * h;
-          float ym[4], yv[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t r = mix((uint32_t)(o + e) * 0x85297A4Du + key);
-            ym[e] = round_e4m3<false>(m[4 * h + e] * inv_m, (float)(r & 0xFFFFu) * 0x1p-16f);
-            yv[e] = round_e4m3<true>(v[4 * h + e] * inv_v, (float)(r >> 16) * 0x1p-16f);
-          }
-          store_code4((uint8_t*)t.m[i] + o, n, pack4_e4m3_grp(ym[0], ym[1], ym[2], ym[3]));
-          store_code4((uint8_t*)t.v[i] + o, n, pack4_e4m3_grp(yv[0], yv[1], yv[2], yv[3]));
-        }
-      }
+      store_code4((uint8_t*)t.m[i] + o, n, pack4_e4m3_grp(ym[0], ym[1], ym[2], ym[3]));
+      store_code4((uint8_t*)t.v[i] + o, n, pack4_e4m3_grp(yv[0], yv[1], yv[2], yv[3]));
     }
   }
 }
@@ -245,8 +242,7 @@ hipError_t adamw(const AdamBatch& b, const AdamStep& a, bool g_bf16, bool bits8,
     t.last[i] = b.last[i];
   }
   t.cum[b.n] = b.cum[b.n];
-  const int chunks = b.cum[b.n], most = device_cu_count() * 8;
-  const dim3 grid(chunks < most ? chunks : most), block(kAdamThreads);
+  const dim3 grid(b.cum[b.n]), block(kAdamThreads);
   if (bits8) {
     if (g_bf16) hipLaunchKernelGGL((k_adamw<N, true, true>), grid, block, 0, st, t, a);
     else hipLaunchKernelGGL((k_adamw<N, false, true>), grid, block, 0, st, t, a);

@@ -1091,15 +1091,6 @@ bool adamw_overlaps(const fp8q_adamw_tensor* t, int64_t n, int bits) {
   return bits == 8 && (over(&fp8q_adamw_tensor::m_scale, scales) || over(&fp8q_adamw_tensor::v_scale, scales));
 }
 
-// Elements that a block takes at a time: one step of it while that gives no more
-// blocks than run at once, so that a few small tensors are worked on side by side
-// (60 tensors up to 100000 elements: 10 us with 4 steps a block).
-int adamw_chunk(const fp8q_adamw_tensor* t, int64_t n) {
-  int64_t blocks = 0;
-  for (int64_t i = 0; i < n; ++i) blocks += cdiv(t[i].len, fp8q::kAdamStep);
-  return blocks <= 8 * fp8q::device_cu_count() ? fp8q::kAdamStep : fp8q::kAdamChunk;
-}
-
 }  // namespace
 
 extern "C" {
@@ -1115,10 +1106,9 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int64_t n, fp8q_dtype g
   if (n == 0) return FP8Q_OK;
   if (!tensors) return FP8Q_ERR_NULL;
   if (!aligned4(norm)) return FP8Q_ERR_ALIGN;
-  int64_t chunks = 0;  // of all tensors: counted in 32 bits
   for (int64_t i = 0; i < n; ++i) {
     const fp8q_adamw_tensor& t = tensors[i];
-    if (t.len < 0 || (chunks += cdiv(t.len, fp8q::kAdamChunk)) > kMaxDim / 2) return FP8Q_ERR_SHAPE;
+    if (t.len < 0 || t.len > fp8q::kMaxAdamChunks * fp8q::kAdamChunk) return FP8Q_ERR_SHAPE;
     if (t.len == 0) continue;
     if (!t.p || !t.g || !t.m || !t.v || (bits == 8 && (!t.m_scale || !t.v_scale))) return FP8Q_ERR_NULL;
     if (!aligned4(t.p) || !aligned_to(t.g, esize(gt)) || !aligned_to(t.copy, 2)) return FP8Q_ERR_ALIGN;
@@ -1148,15 +1138,14 @@ fp8q_status fp8q_adamw(const fp8q_adamw_tensor* tensors, int64_t n, fp8q_dtype g
     b.n = 0;
     b.cum[0] = 0;
     a.place = (uint32_t)i;
-    const int64_t end = n - i < fp8q::kMaxAdamTensors ? n : i + fp8q::kMaxAdamTensors;
-    a.chunk = adamw_chunk(tensors + i, end - i);
-    for (; i < end; ++i) {
+    for (; i < n && b.n < fp8q::kMaxAdamTensors; ++i) {
       const fp8q_adamw_tensor& t = tensors[i];
-      const int64_t c = cdiv(t.len, a.chunk);
+      const int64_t c = cdiv(t.len, fp8q::kAdamChunk);
+      if (b.cum[b.n] + c > fp8q::kMaxAdamChunks) break;
       const int k = b.n++;
       b.p[k] = t.p; b.g[k] = t.g; b.m[k] = t.m; b.v[k] = t.v;
       b.m_scale[k] = t.m_scale; b.v_scale[k] = t.v_scale; b.copy[k] = t.copy;
-      b.last[k] = (uint16_t)(t.len - (c - 1) * a.chunk);
+      b.last[k] = (uint16_t)(t.len - (c - 1) * fp8q::kAdamChunk);
       b.cum[k + 1] = b.cum[k] + (int)c;
     }
     if (b.cum[b.n] > 0 && fp8q::launch_adamw(b, a, gt == FP8Q_BF16, bits == 8, stream) != hipSuccess) return FP8Q_ERR_LAUNCH;

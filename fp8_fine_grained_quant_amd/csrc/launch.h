@@ -250,8 +250,8 @@ hipError_t launch_rms_norm_bwd(const NormRows& a, const void* dy, int64_t ld_dy,
 
 // ---------------------------------------------------------------- AdamW
 constexpr int kMaxAdamTensors = 60;  // per launch: the table travels in the kernel's arguments, 4 KB at most
-constexpr int kAdamStep = 2048;      // elements that a block takes in one step
-constexpr int kAdamChunk = 4 * kAdamStep;  // and of one tensor at a time, where there are blocks enough
+constexpr int kAdamChunk = 2048;     // elements of a tensor that a block takes
+constexpr int64_t kMaxAdamChunks = ((int64_t(1) << 32) - 1) / 256;  // per launch: its threads are counted in 32 bits
 // Consecutive tensors of a call; empty ones among them have no chunk.
 template <int N>
 struct AdamTable {
@@ -274,7 +274,6 @@ struct AdamStep {
   float root;                        // 1 / sqrt(1 - beta2^t)
   float eps;
   uint32_t seed_lo, seed_hi;         // of the random numbers, with
-  int chunk;                         // elements of one tensor a block takes at a time
   uint32_t place;                    // the place of the table's first tensor in the call's list
   const float* norm;                 // of all gradients, or NULL
   double max_norm;

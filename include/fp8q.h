@@ -773,11 +773,11 @@ fp8q_status fp8q_grouped_gemm_dgrad_swiglu(const uint8_t* dyq, const float* dys,
  * 0xB2D05E13, x ^ x >> 16: the same seed repeats a step, another one for every step
  * keeps the roundings independent.  A gradient that is not finite makes its group
  * of 128 states NaN.
- * 0 <= beta < 1, eps >= 0, max_norm >= 0 (inf: no clipping).  Tensors start at any
- * element and must not overlap each other (a list of parameters, states, scales or
- * copies that holds memory twice is refused, FP8Q_ERR_SHAPE, as are numbers of the
- * step that FP32 does not hold).  The numbers of the step are read at the call: a captured call
- * repeats the same step.
+ * 0 <= beta < 1, eps >= 0, max_norm >= 0 (inf: no clipping), len <= 2^35 - 2048.
+ * Tensors start at any element and must not overlap each other (a list of
+ * parameters, states, scales or copies that holds memory twice is refused,
+ * FP8Q_ERR_SHAPE, as are numbers of the step that FP32 does not hold).  The numbers
+ * of the step are read at the call: a captured call repeats the same step.
  */
 typedef struct {
   float* p;
