@@ -1,6 +1,6 @@
 // The gated feed-forward block and its gradient of a few hundred rows (gfx950),
-// in all or an expert: too many for the kernel of few rows, and too few for the 256-row tiles to give
-// every compute unit one.
+// in all or an expert: too many for the kernel of few rows, and too few for the
+// 256-row tiles to give every compute unit one.
 //
 // Tiles of 16 TM rows (32, 64 or 128) by 64 TN rows of B: of the block TN is 4, 128
 // gate and the 128 up rows of the same outputs (a whole group of h's codes); of the
@@ -17,9 +17,10 @@
 //
 // 512 rows of 2048 x 7168 with gate and up kept: 31 us (the large tiles 72), 1024
 // rows 38 (75), 2048 rows 62 (76); their gradients 20 (55), 26 (57), 41 (59).  The
-// time goes with the loads that a compute unit's waves put out, 37 to 49 KB a chunk
-// of the block: half of B's rows left away change it by 7 parts in 100, more stages
-// by nothing, and a chunk's loads one by one behind its matrix instructions instead
+// time of a chunk is that of the loads to LDS that a compute unit's waves put out
+// for it, about 27 cycles each (24 to 53 loads; with 128 rows the block's matrix
+// instructions take longer).  More stages change nothing, nor does reading all
+// fragments first; a chunk's loads one by one behind its matrix instructions instead
 // of together before them take 33 us instead of 37 with 64 rows, 53 instead of 65
 // with 128 (a chunk's fragments read at its own begin: 54 and 91).
 
