@@ -18,7 +18,7 @@
 // 512 rows of 2048 x 7168 with gate and up kept: 31 us (the large tiles 72), 1024
 // rows 38 (75), 2048 rows 62 (76); their gradients 20 (55), 26 (57), 41 (59).  The
 // time of a chunk is that of the loads to LDS that a compute unit's waves put out
-// for it, about 27 cycles each (24 to 53 loads; with 128 rows the block's matrix
+// for it, about 27 cycles each (24 to 52 loads; with 128 rows the block's matrix
 // instructions take longer).  More stages change nothing, nor does reading all
 // fragments first; a chunk's loads one by one behind its matrix instructions instead
 // of together before them take 33 us instead of 37 with 64 rows, 53 instead of 65
