@@ -142,6 +142,7 @@ def test_adamw(lib):
                 dict(wd=inf), dict(lr=1e300), dict(eps=1e39), dict(most=-1.0), dict(most=nan)):
         assert adamw_call(lib, one(), **bad) == SHAPE, bad
     assert adamw_call(lib, one(len=-1)) == SHAPE and adamw_call(lib, one(len=1 << 45)) == SHAPE
+    assert adamw_call(lib, one(len=(1 << 35) - 2047)) == SHAPE  # more than a launch's blocks hold
     for name in ("p", "g", "m", "v"):
         assert adamw_call(lib, one(**{name: None})) == NULL, name
     for name in ("ms", "vs"):
