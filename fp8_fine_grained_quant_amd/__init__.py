@@ -1039,7 +1039,7 @@ MAX_NORM_COLS = 16384
 def rms_norm(x, weight, residual=None, eps=1e-6, stream=None):
     """Root-mean-square norm of the rows of x, or of x + residual: (y, sum,
     rstd).  sum is the stream that goes on (None without a residual), rstd
-    [rows] FP32 is for the gradient.  Rows and codes made here start on 64-byte
+    [rows] FP32 is for the gradient (zeros for rows of no columns).  Rows and codes made here start on 64-byte
     segments, as those of moe_dispatch."""
     y, _, _, total, rstd = _native().rms_norm(x, weight, residual, eps, None, None, None, None, None, _ROWS, stream)
     return y, total, rstd

@@ -657,6 +657,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       sum = &own_sum;
     }
     rstd = &given_or(nullptr, own_rstd, {rows}, at::kFloat, x);
+    if (cols == 0) own_rstd.zero_();  // the entry point has nothing to do
   }
   const int64_t ld = stride(x), ld_r = residual ? stride(*residual) : 0, ld_s = residual ? stride(*sum) : 0,
                 ld_y = out.ld_rows(), ld_q = out.ld_q(), ld_sc = out.ld_scale();

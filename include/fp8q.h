@@ -662,7 +662,8 @@ int64_t fp8q_grad_clip_workspace(int64_t n);
  *   rstd   : [rows] FP32, for the gradient
  * Rows start at any element and have any stride, as those of the routing entry
  * points; cols <= 16384.  Squares are summed in FP32: a row's sum of squares
- * has to be finite there.  With eps = 0 a row of zeros gives NaN.
+ * has to be finite there.  With eps = 0 a row of zeros gives NaN.  With cols = 0
+ * nothing is written, rstd neither.
  */
 fp8q_status fp8q_rms_norm(const void* x, fp8q_dtype t, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
                           int64_t ld_r, const float* weight, float eps, void* y, int64_t ld_y, uint8_t* q, int64_t ld_q,
