@@ -998,7 +998,8 @@ def fp8q_rms_norm_bwd(dy, x, weight, rstd, dweight, workspace, dx=None, q=None, 
 
 def gemm_swiglu_workspace(rows, width, inner, codes):
     """Bytes of workspace that fp8q_gemm_swiglu needs on the current device for
-    x [rows, inner] and a block of `width` (codes: q is wanted)."""
+    x [rows, inner] and a block of `width` (codes: q is wanted).  With codes it is
+    above 0 for just the sizes of the kernel for few rows, whose products are exact."""
     n = load_library().fp8q_gemm_swiglu_workspace(rows, width, inner, int(bool(codes)))
     if n < 0:
         raise ValueError(f"{rows} rows of {inner}, width {width}: out of range")

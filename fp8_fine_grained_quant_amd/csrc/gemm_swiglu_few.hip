@@ -221,8 +221,14 @@ int few_tiles(int64_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : M <= 64 ? 4 : 8; }
 // By the times of the kernels in ns, of rounds of workgroups: here 4 us and 40 + 31
 // mt ns a chunk (8, 32, 64 and 128 rows of 2048 x 7168: 7.3, 8.7, 12.1 and 19.4 us;
 // tiles of 32 rows take 28 there up to 256 rows, the large ones 50 to 70).  Up to 16
-// rows the small tiles are not asked: what is generated for a few sequences has the
-// exact products' accuracy.
+// rows only the large tiles' time is asked, not the small ones', so that what is
+// generated for a few sequences mostly has the exact products' accuracy: with K = 128
+// up to a width of 4096, with K = 1024 of 8192 (but for 6272), with K = 7168 of 22528
+// (and at some widths above), from K = 16384 on of any.  Wider blocks fill the device
+// with FP8 tiles (the small ones, once they are not taken here), which are faster
+// with a short K: 8 rows of 8192, 16384 and 32768 x 128 take 5.4 us (here 7.2, 12 and
+// 23), of 24576 x 1024 12 (24), of 32768 x 7168 80 (88), but of 24576 x 4096 45 (40)
+// and of 28672 x 8192 82 (79).
 bool swiglu_few(int64_t M, int64_t N, int64_t K) {
   const int64_t mt = few_tiles(M), nk = K / 128, cus = device_cu_count();
   const int64_t rounds = ((M + 16 * mt - 1) / (16 * mt) * (N / kFewCols) + cus - 1) / cus;

@@ -708,6 +708,9 @@ int64_t fp8q_rms_norm_bwd_workspace(int64_t rows, int64_t cols);
  * the device without a tile, a kernel for few rows runs, with the accuracy of
  * fp8q_gemm_fprop_exact (by the sizes and the device's compute units alone: with
  * K = 7168 up to 128 rows of a block of width 2048 and up to 16 of one of 16384).
+ * How few the rows are does not decide it alone: a wide block has tiles enough with
+ * one row too (K = 128: from width 4224 on, K = 7168: 22656 to 32768).  It runs
+ * for the sizes of which fp8q_gemm_swiglu_workspace(M, N, K, 1) is above 0.
  * Rules: N % 128 == 0, K % 128 == 0, K <= 131072, any M >= 0; xq, wq, h, gu, q
  * 16-byte aligned with row strides that are multiples of 16 bytes.
  */
