@@ -1130,9 +1130,11 @@ def adamw(params, grads, exp_avg, exp_avg_sq, step, lr, betas=(0.9, 0.95), eps=1
     grads: FP32 or BF16.  exp_avg, exp_avg_sq: FP32, or with scales (two lists
     of FP32 [ceil(n / 128)]) the E4M3 codes (uint8, or torch's float8_e4m3fn) of
     the first moment and of the second one's root, rounded at random by `seed` (another one for every
-    step).  norm: the gradients' norm (0-dim FP32 on the GPU, from grad_clip with
+    step; the root's mean is kept, so that the held second moment is 2 to 5 %
+    above the one in 32 bits).  norm: the gradients' norm (0-dim FP32 on the GPU, from grad_clip with
     max_norm=inf), by which the step clips them to max_norm.  copies: BF16
-    tensors that receive the new parameters."""
+    tensors that receive the new parameters.  step, lr, seed and the other numbers
+    are read at the call: a captured call repeats the same step."""
     m_scales, v_scales = scales if scales is not None else (None, None)
     beta1, beta2 = betas
     _native().adamw(params, grads, exp_avg, exp_avg_sq, m_scales, v_scales, copies, lr, beta1, beta2, eps, weight_decay,

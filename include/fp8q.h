@@ -775,8 +775,13 @@ fp8q_status fp8q_grouped_gemm_dgrad_swiglu(const uint8_t* dyq, const float* dys,
  * place i in its tensor, key = mix(mix(seed_lo + 0x9E3779B1 * tensor) + seed_hi),
  * where mix(x) in 32 bits is x = (x ^ x >> 16) * 0x6C8E9CF5, x = (x ^ x >> 15) *
  * 0xB2D05E13, x ^ x >> 16: the same seed repeats a step, another one for every step
- * keeps the roundings independent.  A gradient that is not finite makes its group
- * of 128 states NaN.
+ * keeps the roundings independent.  The rounding keeps the mean of what it rounds,
+ * m and sqrt(v); the mean of the held root's square, which the next step takes for v,
+ * is above v by the rounding's variance.  For gradients without a trend the held v
+ * is 1.02 to 1.03 times the FP32 state's in the mean with beta2 = 0.95 and 1.05 with
+ * 0.99 and 0.999, and the mean size of a step, in which m's rounding counts as well,
+ * 1.007 to 1.016 times.  A gradient that is not finite makes its group of 128 states
+ * NaN.
  * 0 <= beta < 1, eps >= 0, max_norm >= 0 (inf: no clipping), len <= 2^35 - 2048.
  * Tensors start at any element and must not overlap each other (a list of
  * parameters, states, scales or copies that holds memory twice is refused,
