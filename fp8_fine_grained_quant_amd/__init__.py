@@ -194,7 +194,9 @@ _TILES = {"auto": 0, "256x128": 1, "256x256": 2}
 
 def set_gemm_tile(tile):
     """Force the GEMMs' workgroup tile ("256x128", "256x256") or give the
-    choice back to the library ("auto"); results are bit-identical."""
+    choice back to the library ("auto"); results are bit-identical.  A forced tile
+    keeps the gated block and its gradient from their tiles of 32 to 128 rows, not
+    from the kernel for few rows."""
     _check(load_library().fp8q_set_gemm_tile(_TILES[tile]), "fp8q_set_gemm_tile")
 
 

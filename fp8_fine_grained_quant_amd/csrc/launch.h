@@ -105,8 +105,8 @@ struct GemmArgs {
 hipError_t launch_gemm(const GemmArgs& a, hipStream_t st);
 
 // Workgroup tile of the block-scaled GEMMs: 0 = chosen by problem size,
-// 1 = 256 x 128, 2 = 256 x 256 (fp8q_set_gemm_tile; both tiles give the same
-// result bits).
+// 1 = 256 x 128, 2 = 256 x 256 (fp8q_set_gemm_tile; all tiles give the same
+// result bits, the gated block's of fewer rows, which only 0 takes, too).
 int gemm_tile_setting();
 // Compute units of the current device, queried once per device.
 int device_cu_count();

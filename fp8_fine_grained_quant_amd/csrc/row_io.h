@@ -1,5 +1,5 @@
-// Row access shared by the MoE row kernels and gradient clipping: elements of a
-// row as 16-byte accesses at ANY element alignment.  gfx950 global
+// Row access shared by the MoE row kernels, gradient clipping, the norm and AdamW:
+// elements of a row as 16-byte accesses at ANY element alignment.  gfx950 global
 // memory instructions take multi-dword accesses at any byte address, so rows
 // whose length is odd use the same instructions as aligned ones; only the
 // alignment the compiler may assume differs.

@@ -44,9 +44,12 @@
  *   - The FP8 and MX GEMMs pick a 256x128 or a 256x256 workgroup tile by
  *     problem size (the wide one when its grid has more tiles than half the
  *     device's compute units and the output width is a multiple of 256).
- *     Both run the same arithmetic in the same order, so the choice never
- *     changes a result bit.  fp8q_set_gemm_tile (below) forces either tile
- *     for tests and measurement.
+ *     The gated block and its gradient also have tiles of 32, 64 and 128 rows,
+ *     taken where their estimated time is lower.  All run the same arithmetic
+ *     in the same order, so the choice never changes a result bit.
+ *     fp8q_set_gemm_tile (below) forces one of the two large tiles for tests and
+ *     measurement.  (The gated block's kernel for few rows has other bits; the
+ *     sizes alone decide on it, whatever tile is forced.)
  *   - Arguments are validated on the host before anything is enqueued; a bad
  *     argument returns its status and enqueues nothing.  A zero-size call is
  *     a no-op returning FP8Q_OK.  A launch failure reported by the HIP runtime
@@ -93,7 +96,10 @@ const char* fp8q_status_string(fp8q_status s);
 
 /* Process-wide choice of the GEMMs' workgroup tile, for tests and
  * measurement: 0 = by problem size (the default), 1 = 256x128, 2 = 256x256
- * where the output width allows it.  The tiles give bit-identical results, so
+ * where the output width allows it.  1 and 2 also keep the gated block and its
+ * gradient from their tiles of fewer rows (the block's large tile is the same
+ * with both: 256 rows of 128 gate and 128 up columns); its kernel for few rows is
+ * not a matter of this choice.  The tiles give bit-identical results, so
  * this changes timing only.  It is the library's one piece of state: calls on
  * other threads see the new value from their next launch.  Returns
  * FP8Q_ERR_SHAPE (and changes nothing) for any other value. */
