@@ -24,12 +24,14 @@
 // Bound by memory: every value is read and written once, 28 bytes an element
 // with FP32 gradients and states, 16.1 with 8-bit states and two more for a BF16
 // copy.  Parameters, gradients, copies and FP32 states pass the caches: 235M
-// parameters with 8-bit states and copies 728 us, 5.9 TB/s (790 through them,
-// 770 with only the stores past them); 200M with FP32 states 972 us, 5.8 TB/s
-// (1043).  A block has one piece of a tensor, 8 elements a thread, and ends: what
-// the device holds is then made up by the pieces that begin as others end (2048
-// blocks that took 8192 elements at a time: 816 and 1045 us; 200 tensors of 100 to
-// 2000000 elements 160 us against 139, whose last blocks ran alone).
+// parameters with 8-bit states and copies 735 us a pass (724 to 766 by card and
+// timer), 5.8 TB/s; 200M with FP32 states 972, 5.8 TB/s.  In turn with the other
+// ways: 724 and 977 us, all through the caches 794 and 1052 (only the stores past
+// them 770 where that was 728).  A block has one piece of a tensor, 8 elements a
+// thread, and ends: what the device holds is then made up by the pieces that begin
+// as others end (in turn, 2048 blocks that took 8192 elements at a time 816 and 1045
+// us against 728 and 972; 200 tensors of 100 to 2000000 elements, whose last blocks
+// ran alone, 160 against 139).
 
 #include "launch.h"
 #include "row_io.h"

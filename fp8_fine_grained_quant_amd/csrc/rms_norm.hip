@@ -19,10 +19,13 @@
 // registers and writes it once, and a second launch adds the blocks' parts (in
 // a fixed order; no atomics).
 //
-// 4096 BF16 rows of 7168 with residual, rows and codes: 53.6 us, 4.9 TB/s, where a
+// 4096 BF16 rows of 7168 with residual, rows and codes: 54 us, 4.9 TB/s, where a
 // copy of that many bytes has 5.4; gradient of 16384 rows of 7168 with the
-// stream's gradient, rows and codes: 193 us, 5.5 TB/s (a copy: 5.0); of 2999 FP32
-// rows of 1027: 13.2 us (11 and 3), bound by the latency of three rounds of rows.
+// stream's gradient, rows and codes: 193 to 197 us (the profiler has 206 + 5),
+// 5.5 TB/s (a copy: 5.0); of 2999 FP32 rows of 1027: 13.2 us (9.4 and 3.8), bound by
+// the latency of three rounds of rows; of 32768 BF16 rows of 128 13.4 us, twice the
+// bytes' time: two rounds of rows, the block's 64 rows' sums of dw one after the
+// other, and the second launch (3).
 
 #include "launch.h"
 #include "row_io.h"
@@ -359,8 +362,9 @@ int64_t norm_blocks(int64_t rows, int threads, int waves) {
 
 // Whether `matrices` matrices of the rows' size are too much for the caches (256
 // MB, and what follows finds its rows there if they fit): past them, the norm of
-// 16384 rows of 7168 with residual and codes takes 158 us (166 through them) and
-// its gradient 195 (205); with 4096 rows it is 51 (49), with 2048 29 (24).
+// 16384 rows of 7168 with residual takes 161 us with codes (169 through them), 192
+// with rows and codes (209), and its gradient 197 (206); with 4096 rows and codes it
+// is 51 (49), with 2048 29 (24).
 bool past_caches(const NormRows& a, int matrices) {
   return a.rows * a.cols * (a.bf16 ? 2 : 4) * matrices > ((int64_t)512 << 20);
 }
