@@ -650,6 +650,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   contiguous({&weight, rstd});
   const fp8q_dtype type = type_of(x);
   Tensor own_sum, own_rstd;
+  const hipStream_t st = stream_of(a[10], device);
   if (make_outputs) {
     out.allocate(small(a[9]), rows, cols, x);
     if (residual) {
@@ -661,7 +662,6 @@ PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const int64_t ld = stride(x), ld_r = residual ? stride(*residual) : 0, ld_s = residual ? stride(*sum) : 0,
                 ld_y = out.ld_rows(), ld_q = out.ld_q(), ld_sc = out.ld_scale();
-  const hipStream_t st = stream_of(a[10], device);
   check(unlocked([&] {
           return block.rms_norm(data<void>(x), type, rows, cols, ld, data<void>(residual), ld_r, data<float>(weight),
                                 eps, data<void>(out.rows), ld_y, data<uint8_t>(out.q), ld_q, data<float>(out.scale),
